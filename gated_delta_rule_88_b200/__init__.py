@@ -30,6 +30,17 @@ Entry points (same names as the C ABI):
     kda_chunk_bwd(..., cu_seqlens=None, saved=None): the same gradients by the chunked form
                      (bf16, dk = dv = 128; tensor cores)
     kda_state_affine(M, B, S_in, out=None) -> S_out
+    kda_latent_attn(q, cache, page_table, kv_lens, dv=512, cu_seqlens=None, out=None, lse=None,
+                    scale=None, causal=True) -> (out, lse): attention of the new
+                    tokens over the paged latent cache of a full-attention layer
+    kda_latent_append(kv, cache, page_table, kv_lens, q_pe=None, q=None, freqs=None,
+                    cu_seqlens=None, interleaved=False, scale=1.0): the new tokens
+                    into their pages, with rotary positions
+    kda_rope(x, positions, freqs, out=None, offset=0, interleaved=False, inverse=False,
+                    scale=1.0) -> out: rotary positions, and their gradient
+    kda_pages_copy(pool, src, dst, planes=False): pages (or state slots) forked,
+                    exchanged, cleared
+    kda_pages_compact(pool, pages, planes=False, out=None) -> new_pages
     kda_get_device_error(stream=None) -> int
     kda_selftest_bounded_wait(limit=1000): one CTA's bounded wait that always
                      runs out (sets device error code 1; no fault)
@@ -47,6 +58,7 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_ex", "kda_chunk_fwd_host", "kda_chunk
            "kda_recurrent_step_ex", "kda_recurrent_steps", "kda_gated_rmsnorm", "kda_state_affine",
            "kda_recurrent_bwd", "kda_chunk_bwd", "kda_chunk_fwd_save", "kda_chunk_saved_bytes",
            "kda_chunk_bwd_saved",
+           "kda_latent_attn", "kda_latent_append", "kda_rope", "kda_pages_copy", "kda_pages_compact",
            "kda_get_device_error", "kda_selftest_bounded_wait",
            "KDAError",
            "KDA_QK_L2NORM", "KDA_BETA_SIGMOID", "KDA_STEPS_CHUNK",
@@ -112,6 +124,14 @@ def load_library():
         lib.kda_chunk_saved_bytes.argtypes = [i] * 5
         lib.kda_chunk_saved_bytes.restype = ll
         lib.kda_state_affine.restype = i
+        f, u = ctypes.c_float, ctypes.c_uint
+        lib.kda_latent_attn.argtypes = [vp] * 7 + [i] * 8 + [ll, f, u, i, vp]
+        lib.kda_latent_append.argtypes = [vp] * 8 + [i] * 8 + [ll] * 4 + [u, f, i, vp]
+        lib.kda_rope.argtypes = [vp] * 4 + [ll] + [i] * 4 + [ll] * 2 + [u, f, i, vp]
+        lib.kda_pages_copy.argtypes = [vp] * 3 + [i] * 3 + [ll, vp]
+        lib.kda_pages_compact.argtypes = [vp] * 3 + [ll, i, i, ll, vp]
+        for fn in ("kda_latent_attn", "kda_latent_append", "kda_rope", "kda_pages_copy", "kda_pages_compact"):
+            getattr(lib, fn).restype = i
         lib.kda_get_device_error.argtypes = [vp, ctypes.POINTER(i)]
         lib.kda_selftest_bounded_wait.argtypes = [ctypes.c_uint, vp]
         lib.kda_selftest_bounded_wait.restype = i
@@ -533,6 +553,217 @@ def kda_state_affine(M, B, S_in, out=None):
     with torch.cuda.device(dev):
         rc = lib.kda_state_affine(_dptr(M), _dptr(B), _dptr(S_in), _dptr(out), count, dk, dv,
                                   _stream_handle(dev))
+    _check(rc)
+    return out
+
+
+_ATTN_FULL, _ROPE_INTERLEAVED, _ROPE_INVERSE = 8, 16, 32
+
+
+def _paged_args(who, T, cache, page_table, kv_lens, cu_seqlens, dev, dt, dk):
+    """Checks the cache's arrays; (num_seqs, num_pages, page_size, max_pages, page_stride)."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != dk:
+        raise ValueError(f"{who}: cache must be [num_pages, page_size, {dk}]")
+    if cache.device != dev or cache.dtype != dt:
+        raise TypeError(f"{who}: cache must be {dt} on {dev}")
+    if cache.stride(2) != 1 or cache.stride(1) != dk:
+        raise ValueError(f"{who}: the rows of a page must be contiguous")
+    _need(page_table, "page_table", dev, torch.int32)
+    _need(kv_lens, "kv_lens", dev, torch.int32)
+    N = kv_lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != N or kv_lens.dim() != 1:
+        raise ValueError(f"{who}: page_table must be [num_seqs, max_pages] and kv_lens [num_seqs]")
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", dev, torch.int32)
+        if tuple(cu_seqlens.shape) != (N + 1,):
+            raise ValueError(f"{who}: cu_seqlens must be [{N + 1}]")
+    elif N == 0 or T % N:
+        raise ValueError(f"{who}: without cu_seqlens the tokens must divide evenly over the sequences")
+    # (a pool of one page may report any stride)
+    stride = cache.stride(0) if cache.shape[0] > 1 else cache.shape[1] * dk
+    return N, cache.shape[0], cache.shape[1], page_table.shape[1], stride
+
+
+def kda_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=None, out=None, lse=None,
+                    scale: float | None = None, causal: bool = True):
+    """Attention of each sequence's new tokens over the paged latent cache that
+    already holds them.  q [T,H,dk] bf16; cache [num_pages,page_size,dk] (pages
+    may be strided), its first dv channels the values; page_table
+    [N,max_pages], kv_lens [N] (new tokens included), cu_seqlens [N+1] or None
+    (T / N tokens each), all int32.  scale: default dk ** -0.5.  causal: a token
+    sees the keys up to its own position, else all of its sequence's.
+    Returns (out [T,H,dv], lse [T,H] fp32); allocated here, rows behind the
+    last sequence are unspecified."""
+    lib = load_library()
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("kda_latent_attn needs CUDA tensors (no CPU path)")
+    if q.dim() != 3:
+        raise ValueError("q must be [T,H,dk]")
+    T, H, dk = q.shape
+    _need(q, "q", dev)
+    N, pages, psize, mp, ps = _paged_args("kda_latent_attn", T, cache, page_table, kv_lens, cu_seqlens, dev, q.dtype, dk)
+    if out is None:
+        out = torch.empty(T, H, dv, dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", dev, q.dtype)
+        if tuple(out.shape) != (T, H, dv):
+            raise ValueError(f"out must be [{T},{H},{dv}]")
+    if lse is None:
+        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", dev, torch.float32)
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"lse must be [{T},{H}]")
+    if T == 0:
+        return out, lse
+    with torch.cuda.device(dev):
+        rc = lib.kda_latent_attn(_dptr(q), _dptr(cache), _dptr(page_table), _dptr(kv_lens), _dptr(cu_seqlens),
+                                 _dptr(out), _dptr(lse), T, H, dk, int(dv), N, pages, psize, mp, ps,
+                                 float(dk ** -0.5 if scale is None else scale), 0 if causal else _ATTN_FULL,
+                                 _dtype_code(q), _stream_handle(dev))
+    _check(rc)
+    return out, lse
+
+
+def kda_latent_append(kv, cache, page_table, kv_lens, q_pe=None, q=None, freqs=None, cu_seqlens=None,
+                      interleaved: bool = False, scale: float = 1.0) -> None:
+    """The new tokens' latents kv [T,dk] (tokens may be strided) into their
+    pages of ``cache``; with freqs [rot/2] fp32 their last rot channels are
+    turned by the token's position, and q_pe [T,H,rot] (tokens and heads may be
+    strided) likewise into q[..., dk-rot:] of q [T,H,dk].  Other arguments as
+    kda_latent_attn."""
+    lib = load_library()
+    dev = kv.device
+    if dev.type != "cuda":
+        raise ValueError("kda_latent_append needs CUDA tensors (no CPU path)")
+    if kv.dim() != 2 or (kv.shape[0] > 0 and kv.stride(1) != 1):
+        raise ValueError("kv must be [T,dk] with contiguous rows")
+    T, dk = kv.shape
+    N, pages, psize, mp, ps = _paged_args("kda_latent_append", T, cache, page_table, kv_lens, cu_seqlens, dev, kv.dtype, dk)
+    H, rot, ts, hs = 1, 0, 0, 0
+    if freqs is not None:
+        _need(freqs, "freqs", dev, torch.float32)
+        rot = 2 * freqs.numel()
+    if (q_pe is None) != (q is None):
+        raise ValueError("q_pe and q come together")
+    if q_pe is not None:
+        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.device != dev or q_pe.dtype != kv.dtype:
+            raise ValueError(f"q_pe must be [{T},H,rot] {kv.dtype} on {dev}")
+        H = q_pe.shape[1]
+        if freqs is not None and q_pe.shape[2] != rot:
+            raise ValueError(f"q_pe must have {rot} channels, twice as many as freqs")
+        rot = q_pe.shape[2]
+        if q_pe.numel() and q_pe.stride(2) != 1:
+            raise ValueError("the heads of q_pe must be contiguous")
+        ts, hs = q_pe.stride(0) if T > 1 else 0, q_pe.stride(1) if H > 1 else 0
+        if ts == 0 and T > 1 or hs == 0 and H > 1:
+            raise ValueError("q_pe must not be broadcast")
+        _need(q, "q", dev, kv.dtype)
+        if tuple(q.shape) != (T, H, dk):
+            raise ValueError(f"q must be [{T},{H},{dk}]")
+    kvs = kv.stride(0) if T > 1 else 0
+    if T > 1 and kvs == 0:
+        raise ValueError("kv must not be broadcast")
+    if T == 0:
+        return
+    with torch.cuda.device(dev):
+        rc = lib.kda_latent_append(_dptr(kv), _dptr(cache), _dptr(page_table), _dptr(kv_lens), _dptr(cu_seqlens),
+                                   _dptr(q_pe), _dptr(q), _dptr(freqs), T, H, dk, rot, N, pages, psize, mp, ps, kvs,
+                                   ts, hs, _ROPE_INTERLEAVED if interleaved else 0, float(scale), _dtype_code(kv),
+                                   _stream_handle(dev))
+    _check(rc)
+
+
+def kda_rope(x, positions, freqs, out=None, offset: int = 0, interleaved: bool = False, inverse: bool = False,
+             scale: float = 1.0):
+    """Rotary positions on channels [offset, offset + 2 len(freqs)) of x [T,H,d]
+    (bf16 or fp32; tokens may be strided); the other channels are copied.
+    positions int32 [T]; freqs fp32: radians a position of each pair (i, i +
+    len(freqs)), or (2i, 2i + 1) if interleaved.  inverse: the transposed map,
+    i.e. the gradient.  out may be x (in place)."""
+    lib = load_library()
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("kda_rope needs CUDA tensors (no CPU path)")
+    if x.dim() != 3:
+        raise ValueError("x must be [T,H,d]")
+    T, H, d = x.shape
+
+    def stride(t, name):
+        if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+            raise ValueError(f"the heads of {name} must be contiguous")
+        if T > 1 and t.stride(0) == 0:
+            raise ValueError(f"{name} must not be broadcast")
+        return t.stride(0) if T > 1 else H * d
+
+    xs = stride(x, "x")
+    _need(positions, "positions", dev, torch.int32)
+    _need(freqs, "freqs", dev, torch.float32)
+    if tuple(positions.shape) != (T,) or freqs.dim() != 1:
+        raise ValueError(f"positions must be [{T}] and freqs [rot / 2]")
+    if out is None:
+        out = torch.empty(T, H, d, dtype=x.dtype, device=dev)
+    elif tuple(out.shape) != (T, H, d) or out.device != dev or out.dtype != x.dtype:
+        raise ValueError(f"out must be [{T},{H},{d}] {x.dtype} on {dev}")
+    code = _dtype_code(x)
+    if T == 0:
+        return out
+    with torch.cuda.device(dev):
+        rc = lib.kda_rope(_dptr(x), _dptr(positions), _dptr(freqs), _dptr(out), T, H, d, 2 * freqs.numel(), int(offset),
+                          xs, stride(out, "out"), (_ROPE_INTERLEAVED if interleaved else 0) |
+                          (_ROPE_INVERSE if inverse else 0), float(scale), code, _stream_handle(dev))
+    _check(rc)
+    return out
+
+
+def _pool_args(who, pool, planes):
+    """(planes, num_pages, page_bytes) of a contiguous pool [pages, ...] or [planes, pages, ...]."""
+    if not isinstance(pool, torch.Tensor) or pool.device.type != "cuda":
+        raise ValueError(f"{who} needs CUDA tensors (no CPU path)")
+    if pool.dim() < (3 if planes else 2) or not pool.is_contiguous() or pool.numel() == 0:
+        raise ValueError(f"{who}: the pool must be a contiguous, non-empty [{'planes, ' if planes else ''}pages, ...]")
+    n, p = (pool.shape[0], pool.shape[1]) if planes else (1, pool.shape[0])
+    return n, p, pool.numel() // (n * p) * pool.element_size()
+
+
+def kda_pages_copy(pool, src, dst, planes: bool = False) -> None:
+    """Pages of ``pool`` [pages, ...] (planes: [planes, pages, ...], all planes
+    alike) copied within it: page dst[i] <- page src[i] as before the call, or
+    zeros for src[i] = -1.  src, dst int32 [n], n <= 4096; sources and
+    destinations may overlap in any way; the last move to a destination counts.
+    Works on a latent cache and on the state pool of kda_recurrent_steps."""
+    lib = load_library()
+    n, p, nbytes = _pool_args("kda_pages_copy", pool, planes)
+    dev = pool.device
+    _need(src, "src", dev, torch.int32)
+    _need(dst, "dst", dev, torch.int32)
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be [n]")
+    with torch.cuda.device(dev):
+        rc = lib.kda_pages_copy(_dptr(pool), _dptr(src), _dptr(dst), src.numel(), n, p, nbytes, _stream_handle(dev))
+    _check(rc)
+
+
+def kda_pages_compact(pool, pages, planes: bool = False, out=None):
+    """Moves the live pages of ``pool`` to its front and returns their new
+    indexes, in the shape of ``pages`` (int32, any shape: e.g. a whole page
+    table; negative entries are padding; a page may be listed several times).
+    With n distinct live pages, those at n and beyond go to the free indexes
+    below n, both in ascending order.  out may be ``pages``."""
+    lib = load_library()
+    n, p, nbytes = _pool_args("kda_pages_compact", pool, planes)
+    dev = pool.device
+    _need(pages, "pages", dev, torch.int32)
+    if out is None:
+        out = torch.empty_like(pages)
+    else:
+        _need(out, "out", dev, torch.int32)
+        if out.shape != pages.shape:
+            raise ValueError("out must have the shape of pages")
+    with torch.cuda.device(dev):
+        rc = lib.kda_pages_compact(_dptr(pool), _dptr(pages), _dptr(out), pages.numel(), n, p, nbytes,
+                                   _stream_handle(dev))
     _check(rc)
     return out
 

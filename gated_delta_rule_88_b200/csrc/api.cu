@@ -62,15 +62,10 @@ kda_status fail(kda_status s, const char *fmt, ...) {
 }
 }  // namespace kda
 
-namespace {
-using kda::t_msg;
-using kda::fail;
-
+namespace kda {
 kda_status cuda_fail(cudaError_t e, const char *what) {
     return fail(KDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Library-private stream-ordered memory pool per device.  Its release
 // threshold is unbounded, so scratch freed at the end of a call stays
@@ -103,8 +98,13 @@ cudaError_t get_pool(cudaMemPool_t *out, int *sm_count) {
     *sm_count = sms[dev];
     return cudaSuccess;
 }
+}  // namespace kda
 
-}  // namespace
+using kda::aligned16;
+using kda::cuda_fail;
+using kda::fail;
+using kda::get_pool;
+using kda::t_msg;
 
 static kda_status chunk_fwd_device(const void *q, const void *k, const void *v, const float *g,
                                    const float *beta, const float *initial_state,

@@ -20,6 +20,16 @@ extern thread_local char t_msg[512];
 // Records the message for kda_last_error_message() and returns s.
 kda_status fail(kda_status s, const char *fmt, ...);
 
+// The same for a failed CUDA call.
+kda_status cuda_fail(cudaError_t e, const char *what);
+
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// The current device's library-private stream-ordered memory pool and its
+// number of SMs.
+cudaError_t get_pool(cudaMemPool_t *out, int *sm_count);
+
 // kda_chunk_fwd's argument rules (null pointers, sizes, dtype, varlen mode,
 // alignment, problem size), with messages prefixed by fn.  On KDA_OK, *N_out
 // is the number of sequences.  Enqueues nothing.

@@ -129,4 +129,38 @@ cudaError_t launch_chunk_bwd_local(const void *q, const void *k, const void *v, 
                                    const unsigned char *dvn_img, float *dq, float *dk, float *dv,
                                    float *dg, float *dbeta, int *err, cudaStream_t st);
 
+// The paged latent cache's arrays and sizes, shared by its calls (kda.h);
+// page_stride in elements; without cu_seqlens, T / N tokens a sequence.
+struct PagedPlan {
+    const int32_t *page_table, *kv_lens, *cu_seqlens;
+    int T, H, N, num_pages, page_size, max_pages;
+    long long page_stride;
+};
+
+// Attention of the new tokens over the cache (latent_attn.cu): bf16, dv in
+// {256, 512}, dk - dv in {0, 64}.
+cudaError_t launch_latent_attn(const void *q, const void *cache, const PagedPlan &p, void *out, float *lse,
+                               int dk, int dv, float scale, bool full, int *err, cudaStream_t st);
+
+// New tokens into their pages, rotary positions on the last `rot` channels
+// (freqs null: none), and q's rotary part from q_pe (rope.cu).
+cudaError_t launch_latent_append(const void *kv, void *cache, const PagedPlan &p, const void *q_pe, void *q,
+                                 const float *freqs, int dk, int rot, long long kv_stride, long long q_pe_ts,
+                                 long long q_pe_hs, bool interleaved, float scale, bool bf16, int *err,
+                                 cudaStream_t st);
+
+// Rotary positions on channels [offset, offset + rot) of [tokens, H, d] heads.
+cudaError_t launch_rope(const void *x, const int32_t *positions, const float *freqs, void *out,
+                        long long tokens, int H, int d, int rot, int offset, long long x_stride,
+                        long long out_stride, bool interleaved, bool inverse, float scale, bool bf16,
+                        cudaStream_t st);
+
+// Page moves within a pool [planes, num_pages, page_bytes] (pages.cu).
+cudaError_t launch_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int count, int planes,
+                              int num_pages, long long page_bytes, int *err, cudaStream_t st);
+size_t pages_compact_scratch_bytes(int num_pages);
+cudaError_t launch_pages_compact(void *pool, const int32_t *pages, int32_t *new_pages, long long count,
+                                 int planes, int num_pages, long long page_bytes, int *scratch, int sms, int *err,
+                                 cudaStream_t st);
+
 }  // namespace kda

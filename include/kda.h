@@ -20,7 +20,11 @@
  *                       (short queries) on a slot-indexed state pool;
  *   kda_chunk_fwd_host  kda_chunk_fwd on host buffers, copies pipelined
  *                       against the computation;
- *   kda_gated_rmsnorm   the output epilogue (RMSNorm with a sigmoid gate).
+ *   kda_gated_rmsnorm   the output epilogue (RMSNorm with a sigmoid gate);
+ *   kda_latent_attn, kda_latent_append, kda_rope, kda_pages_copy,
+ *   kda_pages_compact   serving the full-attention layers between the KDA
+ *                       layers: a paged latent cache, what writes it, reads it
+ *                       and manages its pages.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers (cudaMalloc'd or any memory the
@@ -454,6 +458,156 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
                                  void *out, float *final_state,
                                  int B, int T, int H, int dk, int dv, int num_seqs,
                                  kda_dtype dtype, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged latent cache of a hybrid's full-attention layers.
+ *
+ * Source: the Kimi Linear paper notes (paper-notes-site) place full-attention
+ * layers with a latent key/value cache between the KDA layers (three KDA
+ * layers to one).  They print no cache layout; paging is a serving layout with
+ * no counterpart in the pages, as the slot pool of kda_recurrent_steps is.
+ *
+ * The cache holds ONE vector a token, shared by all heads (the absorbed form):
+ *   cache       [num_pages, page_size, dk] dtype; its first dv channels are the
+ *               values, all dk channels the keys (the dk - dv last ones, if
+ *               any, carry the rotary positions).  Pages are page_stride
+ *               elements apart (0 selects page_size * dk; a multiple of 8, so
+ *               that a cache may hold several layers' pages side by side).
+ *   page_table  [num_seqs, max_pages] int32: key j of sequence n is row
+ *               j % page_size of page page_table[n][j / page_size].  Only the
+ *               entries that hold keys are read; pages may be shared.
+ *   kv_lens     [num_seqs] int32: cached keys of each sequence, its new tokens
+ *               INCLUDED.
+ *   cu_seqlens  [num_seqs + 1] int32 offsets of each sequence's new tokens on
+ *               the token axis (cu[0] = 0, non-decreasing, cu[num_seqs] <= T;
+ *               clamped to [0, T]; rows behind the last sequence are neither
+ *               read nor written), or NULL: T / num_seqs tokens each.
+ * New token i of a sequence with L of them sits at position kv_len - L + i.
+ * All index arrays are device int32, 4-byte aligned, and read on the device.
+ * A sequence with kv_len < 0, kv_len > max_pages * page_size, or (where the
+ * call reads it) a page outside [0, num_pages) sets the device error word
+ * (kda_get_device_error: code 5); its outputs are not written.
+ * page_size: 16, 32, 64 or 128.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * kda_latent_attn -- attention of each sequence's new tokens (one, or a chunk)
+ * over the paged latent cache, which holds them already (kda_latent_append).
+ *
+ * For each new token at position p and head h, over the keys j <= p (with
+ * KDA_ATTN_FULL: over all kv_len keys):
+ *     x_j = scale * q . cache_j[0:dk],   out = sum_j softmax(x)_j cache_j[0:dv],
+ *     lse = log sum_j e^{x_j}
+ * in fp32, with the probabilities rounded to bf16 for the value product and
+ * out rounded to nearest even.  A token that sees no key (kv_len = 0, or
+ * kv_len < L and i < L - kv_len) gets out = 0, lse = -inf.
+ * Layout: q [T, H, dk] dtype; out [T, H, dv] dtype; lse [T, H] float32 or NULL.
+ * Cache rows at positions >= kv_len are never used and may hold anything;
+ *   rows below it must be finite.
+ * Deterministic: the same call gives the same bits.
+ * Memory: a stream-ordered workspace from the library's pool, of a size that
+ *   depends on the device, H, T / num_seqs and dv only (at most 39 MB).
+ * Supported: KDA_BF16; dv in {256, 512}, dk - dv in {0, 64}; num_seqs <= 65535.
+ *   q, cache, out 16-byte aligned, lse 4.  out must not overlap any input.
+ */
+enum { KDA_ATTN_FULL = 8 };
+kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page_table,
+                           const int32_t *kv_lens, const int32_t *cu_seqlens, void *out,
+                           float *lse, int T, int H, int dk, int dv, int num_seqs, int num_pages,
+                           int page_size, int max_pages, long long page_stride, float scale,
+                           unsigned flags, kda_dtype dtype, void *stream);
+
+/*
+ * Rotary positions, shared by the two calls below.  Of `rot` consecutive
+ * channels, pair i (0 <= i < rot / 2) is turned by the angle
+ *     a = position * freqs[i]      (the product, reduced by whole turns, in fp64)
+ *     (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a)
+ * and rounded once.  Pair i is channels (i, i + rot / 2), or (2i, 2i + 1) with
+ * KDA_ROPE_INTERLEAVED.  freqs: device float32 [rot / 2], so any base and any
+ * scaling for long contexts is the caller's table; scale is their attention
+ * factor.  KDA_ROPE_INVERSE turns by -a: with the same scale this is the
+ * transposed map, i.e. the gradient with respect to the input given the
+ * gradient of the output.
+ */
+enum { KDA_ROPE_INTERLEAVED = 16, KDA_ROPE_INVERSE = 32 };
+
+/*
+ * kda_rope -- rotary positions on channels [offset, offset + rot) of each head;
+ * the other channels are copied.
+ * Layout: x, out [T, H, d] dtype, tokens x_stride / out_stride elements apart
+ *   (0 selects H * d), heads contiguous; positions [T] int32 (any sign); out
+ *   may equal x with the same stride (in place: only the rotated channels are
+ *   touched), else they must not overlap.
+ * Supported: KDA_BF16 or KDA_F32; rot a multiple of 16, d, offset and strides
+ *   multiples of 8, rot <= 1024; pointers 16-byte aligned (positions, freqs 4).
+ */
+kda_status kda_rope(const void *x, const int32_t *positions, const float *freqs, void *out,
+                    long long T, int H, int d, int rot, int offset, long long x_stride,
+                    long long out_stride, unsigned flags, float scale, kda_dtype dtype,
+                    void *stream);
+
+/*
+ * kda_latent_append -- the new tokens' latent vectors into their pages, with
+ * rotary positions, and the rotary part of their queries into q: what a step
+ * does before kda_latent_attn.
+ * Layout: kv [T, dk] dtype, tokens kv_stride elements apart (0 selects dk): the
+ *   first dk - rot channels are stored as they are, the last rot ones turned by
+ *   the token's position.  q_pe [T, H, rot] dtype, elements q_pe_ts between
+ *   tokens (0: H * q_pe_hs) and q_pe_hs between heads (0: rot), turned alike and
+ *   written to q[t, h, dk - rot : dk] of q [T, H, dk]; both NULL: no queries.
+ *   freqs NULL: nothing is turned (layers without positions); rot is then only
+ *   the width of q_pe.  flags: KDA_ROPE_INTERLEAVED or 0.
+ * Tokens of one call must go to distinct cache rows (pages shared by several
+ *   sequences are to be copied before they are written: kda_pages_copy); a
+ *   token at a negative position or without a valid page is not written, nor is
+ *   its part of q, and sets the error word (code 5).
+ * Supported: KDA_BF16 or KDA_F32; rot a multiple of 16 in [16, 1024] (or 0
+ *   without q_pe and freqs), dk and strides multiples of 8; kv, q_pe, q, cache
+ *   16-byte aligned.
+ */
+kda_status kda_latent_append(const void *kv, void *cache, const int32_t *page_table,
+                             const int32_t *kv_lens, const int32_t *cu_seqlens,
+                             const void *q_pe, void *q, const float *freqs, int T, int H, int dk,
+                             int rot, int num_seqs, int num_pages, int page_size, int max_pages,
+                             long long page_stride, long long kv_stride, long long q_pe_ts,
+                             long long q_pe_hs, unsigned flags, float scale, kda_dtype dtype,
+                             void *stream);
+
+/*
+ * kda_pages_copy -- pages copied, exchanged and cleared within a pool: forking
+ * a sequence (copy on write), reordering, freeing.  A pool is any
+ * [planes, num_pages, page_bytes] array: a latent cache (one plane a layer), or
+ * the state pool of kda_recurrent_steps (a page = a slot).
+ *
+ * For each i < count, in every plane: page dst[i] <- page src[i] as it was
+ * BEFORE the call, or zeros if src[i] == -1.  Sources and destinations may
+ * overlap in any way (exchanges, rotations); of several moves to one
+ * destination the last one counts; the other pages stay as they are.
+ * src, dst: device int32 [count].  A move with dst outside [0, num_pages) or src
+ * outside [-1, num_pages) is skipped and sets the device error word (code 3).
+ * Supported: page_bytes a positive multiple of 16, count <= 4096, pool 16-byte
+ *   aligned, planes <= 65535.  No workspace.
+ */
+kda_status kda_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int count, int planes,
+                          int num_pages, long long page_bytes, void *stream);
+
+/*
+ * kda_pages_compact -- the live pages of a pool moved to its front, so that the
+ * rest of it is free: with n distinct live pages, those with an index >= n go,
+ * in ascending order, to the free indexes below n, in ascending order; the
+ * others stay.  pages: device int32 [count], the live pages (e.g. a whole page
+ * table); an entry may appear several times (shared pages), negative entries
+ * are padding.  new_pages [count] receives each entry's new index (padding is
+ * copied); it may equal pages.  Contents of pages that are not live afterwards
+ * are unspecified.  An entry >= num_pages is copied and sets the device error
+ * word (code 3).
+ * Supported: as kda_pages_copy for the pool; num_pages <= 524288; count >= 0.
+ * Memory: 4 * num_pages + 256 bytes from the library's pool.
+ */
+kda_status kda_pages_compact(void *pool, const int32_t *pages, int32_t *new_pages, long long count,
+                             int planes, int num_pages, long long page_bytes, void *stream);
 
 /*
  * kda_selftest_bounded_wait -- a diagnostic for the library's failure path.
