@@ -28,7 +28,7 @@ static kda_status check_plan(const char *fn, const kda::PagedPlan &p, int dk, kd
     if (p.page_stride < (long long)p.page_size * dk || p.page_stride % 8 || p.page_stride > (1LL << 38))
         return fail(KDA_ERR_INVALID_ARG, "%s: page_stride=%lld (a multiple of 8, at least page_size * dk)", fn,
                     p.page_stride);
-    if ((long long)p.T * p.H > 0x7fffffffLL || (long long)p.T * p.H * dk > (1LL << 40))
+    if ((long long)p.T * p.H > 0x7fffff00LL || (long long)p.T * p.H * dk > (1LL << 40))
         return fail(KDA_ERR_INVALID_ARG, "%s: problem too large (T=%d H=%d)", fn, p.T, p.H);
     return KDA_OK;
 }
@@ -57,9 +57,19 @@ kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page
         return fail(KDA_ERR_UNSUPPORTED, "%s: dtype=%d dk=%d dv=%d (supported: bf16, dv in {256, 512}, dk - dv in {0, 64})",
                     fn, (int)dtype, dk, dv);
     if (T == 0) return KDA_OK;
-    cudaError_t e = kda::launch_latent_attn(q, cache, p, out, lse, dk, dv, scale, (flags & KDA_ATTN_FULL) != 0,
-                                            kda::error_word(), (cudaStream_t)stream);
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaMemPool_t mp;
+    int sms = 148;
+    cudaError_t e = kda::get_pool(&mp, &sms);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn memory pool");
+    void *ws = nullptr;
+    e = cudaMallocFromPoolAsync(&ws, kda::latent_attn_workspace(p, dv, sms), mp, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn workspace allocation");
+    e = kda::launch_latent_attn(q, cache, p, out, lse, dk, dv, scale, (flags & KDA_ATTN_FULL) != 0, ws, sms,
+                                kda::error_word(), st);
+    cudaError_t e2 = cudaFreeAsync(ws, st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn launch");
+    if (e2 != cudaSuccess) return cuda_fail(e2, "kda_latent_attn workspace release");
     return KDA_OK;
 }
 
