@@ -3,11 +3,11 @@
 //
 // All heads of a token attend to the same vectors, so a sequence's (token,
 // head) rows are one matrix Q [L * H, dk] against one matrix C [kv, dk] whose
-// first dv columns are also the values.  Per tile of 128 keys and tile of R
+// first dv columns are also the values.  Per tile of 64 keys and tile of R
 // rows (R = 32 or 64):
-//     S^T = C_tile Q^T           (M = 128 keys, N = R rows, K = dk)
-//     P^T = 2^(S^T s - m)        running maximum m per row (column of S^T)
-//     O^T += C_tile[:, :dv]^T P^T   (dv / 128 products, M = 128 channels, N = R, K = 128)
+//     S^T = C_tile Q^T              (M = 64 keys, N = R rows, K = dk)
+//     P^T = 2^(S^T s - m)           running maximum m per row (column of S^T)
+//     O^T += C_tile[:, :dv]^T P^T   (dv / 128 products, M = 128 channels, N = R, K = 64)
 // The transposed form wastes nothing when there are few rows (one token of 32
 // heads is N = 32), keeps O^T in dv / 128 * R TMEM columns (a 128-row
 // tile of O would need all 512), and reads C from shared memory once for both
@@ -20,9 +20,11 @@
 // ranges go as (O, m, l) in fp32 to a workspace and latent_combine_kernel joins
 // them in a fixed order, so results do not depend on timing.
 //
-// Roles: 4 * R / 32 softmax warps (thread = key row of S^T, 32 columns), one TMA
-// warp, one MMA warp.  Every wait is bounded and watches an abort flag; a wait
-// that runs out sets the device error word and the block drains and returns.
+// Roles: four softmax warps (a thread has one key of S^T and half of the rows),
+// a TMA warp, and one warp each to issue the two products, so that S^T of the
+// next tile runs while the softmax of this one does.  Every wait is bounded and
+// watches an abort flag; a wait that runs out sets the device error word and the
+// block drains and returns.
 #include "kernels.h"
 #include "paged.cuh"
 #include "prep_common.cuh"
@@ -33,34 +35,42 @@ namespace {
 
 using namespace sm100;
 
-constexpr int KT = 128;                       // keys of a tile
+constexpr int KT = 64;                        // keys of a tile
 constexpr float TH = 8.f;                     // growth of a maximum (log2) that is let pass
+#ifndef OVH
+#define OVH 2
+#endif
+constexpr int OV = OVH;                       // what a row tile costs besides its key tiles, in key tiles
+#ifndef AHEAD
+#define AHEAD 0
+#endif
 
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((mn ? 1u : 0u) << 15) | ((mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+constexpr int SMEM = 227 * 1024;
+
 template <int R, int DV, bool PE>
 struct Lay {
     static constexpr int MT = DV / 128;                       // stages (128 channels) of a key tile
     static constexpr int NQ = DV / 64 + (PE ? 1 : 0);         // 64-channel pieces of Q
-    static constexpr int SW = 4 * (R / 32);                   // softmax warps
-    static constexpr int NT = 32 * (SW + 2);
-    static constexpr uint32_t STAGE = 32768;                  // 128 keys x 128 channels
-    static constexpr uint32_t PBYTES = KT * R * 2;
-    static constexpr uint32_t Q_OFF = 0;
+    static constexpr int SW = 4;                              // softmax warps
+    static constexpr int NT = 32 * (SW + 3);
+    static constexpr int C = R / 2;                           // rows (columns of S^T) of a softmax thread
+    static constexpr int NPL = R / 32;                        // columns whose statistics a lane holds
+    static constexpr uint32_t HALF = KT * 128;                // 64 keys x 64 channels
+    static constexpr uint32_t STAGE = 2 * HALF;
     static constexpr uint32_t QP = R * 128;                   // one piece of Q
-    // the positional piece of the keys; at R = 64 P^T takes its place once S^T is done
-    static constexpr bool ALIAS = PE && R == 64;
-    static constexpr uint32_t X_OFF = Q_OFF + NQ * QP;
-    static constexpr uint32_t P_OFF = X_OFF + (PE && !ALIAS ? 16384 : 0);
-    static constexpr uint32_t ST_OFF = P_OFF + (ALIAS ? 16384 : PBYTES);
-    static constexpr int NS = (227 * 1024 - 1024 - 4096 - (int)ST_OFF) / (int)STAGE;
-    static constexpr uint32_t MISC = ST_OFF + NS * STAGE;     // barriers and small tables
-    static constexpr uint32_t BYTES = MISC + 4096;
-    // TMEM: two S^T buffers, then O^T
-    static constexpr uint32_t O_COL = 2 * R;
+    static constexpr uint32_t X_OFF = NQ * QP;                // the positional piece of the keys, two buffers
+    static constexpr uint32_t P_OFF = X_OFF + (PE ? 2 * HALF : 0);
+    static constexpr uint32_t ST_OFF = P_OFF + KT * R * 2;
+    static constexpr uint32_t SMALL = 3072;                   // barriers and small tables
+    static constexpr int NS = (SMEM - (int)SMALL - (int)ST_OFF) / (int)STAGE;
+    static constexpr uint32_t MISC = ST_OFF + NS * STAGE;
+    // TMEM: two S^T tiles (lanes +0 and +16 of the same columns), then O^T
+    static constexpr uint32_t O_COL = R;
     static constexpr uint32_t USED = O_COL + MT * R;
     static constexpr uint32_t COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
     // P^T: MN-major, rows of R values swizzled to their width
@@ -73,12 +83,25 @@ struct Lay {
     }
 };
 
+// The small tables behind the stages.
+struct Small {
+    uint64_t full[12], empty[12], x_full[2], x_empty[2], q_full, q_empty, s_full[2], s_free[2], p_full, o_full, drain[2];
+    long long scan[8];
+    long long start_u;           // first unit of the block's row tile, counted over all
+    int start[6];                // sequence, its first token, new tokens, keys; row tile; unit in it
+    uint32_t tmem;
+    int abort_flag;
+    float red[4][64];            // per warp and row
+    float mine[4][64];           // a warp's own copy of a value per row
+};
+static_assert(sizeof(Small) <= 3072, "small tables");
+
 struct Args {
     const int32_t *table, *lens, *cu;
     __nv_bfloat16 *out;
     float *lse;
     float *ws_o, *ws_ml;         // [2 * blocks][R][DV], [2 * blocks][R][2]
-    int4 *meta;                  // [blocks]: first row, rows, further pieces
+    int4 *meta;                  // [2 * blocks]: a split row tile: first row, rows, first block, pieces
     int T, H, N, per, num_pages, page_size, max_pages;
     float sl2;                   // scale * log2 e
     bool full;
@@ -86,21 +109,20 @@ struct Args {
 };
 
 // ---------------------------------------------------------------- schedule
-// A sequence's rows and keys.  tiles_of(i): key tiles of row tile i (at least
-// one: rows that see nothing are written, too).
+// A sequence's rows and keys.  A row tile costs its key tiles (at least one:
+// rows that see nothing are written, too) and OV units more, which come first.
 template <int R>
 struct Seq {
     int first, L, kv, H;         // first token, new tokens, keys (0 tokens if the length is bad)
     bool full, bad;
+    __device__ __forceinline__ void set(const Args &a, int first_, int L_, int kv_) {
+        H = a.H; full = a.full || L_ == 1; first = first_; L = L_; kv = kv_;
+    }
     __device__ __forceinline__ void load(const Args &a, int n) {
-        H = a.H;
-        full = a.full;
         const int b = paged::token_offset(a.cu, n, a.per, a.T), e = paged::token_offset(a.cu, n + 1, a.per, a.T);
-        kv = a.lens[n];
-        first = b;
-        L = max(0, e - b);
-        bad = kv < 0 || (long long)kv > (long long)a.max_pages * a.page_size;
-        if (bad) { L = 0; kv = 0; }
+        const int k = a.lens[n];
+        bad = k < 0 || (long long)k > (long long)a.max_pages * a.page_size;
+        set(a, b, bad ? 0 : max(0, e - b), bad ? 0 : k);
     }
     __device__ __forceinline__ int rows() const { return L * H; }        // T * H < 2^31
     __device__ __forceinline__ int row_tiles() const { return (rows() - 1 + R) / R; }
@@ -110,17 +132,17 @@ struct Seq {
     }
     __device__ __forceinline__ int keys_of(int i) const { return sees(min(rows(), (i + 1) * R) - 1); }
     __device__ __forceinline__ int tiles_of(int i) const { return max(1, (keys_of(i) + KT - 1) / KT); }
-    // row tiles i < C(k) have at most k key tiles
+    // row tiles i < upto(k) have at most k key tiles
     __device__ __forceinline__ int upto(int k) const {
-        const long long tokens = (long long)KT * k - kv + L;             // tokens that see <= 128 k keys
         if (full) return KT * (long long)k >= kv ? row_tiles() : 0;
+        const long long tokens = (long long)KT * k - kv + L;             // tokens that see <= KT k keys
         if (tokens >= L) return row_tiles();
-        return tokens <= 0 ? 0 : (int)(tokens * H / R);
+        return tokens <= 0 ? 0 : (int)((unsigned long long)(tokens * H) / R);
     }
     __device__ __forceinline__ long long units() const {
         const int nt = row_tiles();
         if (nt <= 0) return 0;
-        long long u = 0;
+        long long u = (long long)nt * OV;
         int k = tiles_of(0), done = 0;
         while (done < nt) {
             const int c = min(nt, max(done, upto(k)));
@@ -130,16 +152,18 @@ struct Seq {
         }
         return u;
     }
-    // row tile and key tile of unit u
-    __device__ __forceinline__ void find(long long u, int &i, int &j) const {
+    // row tile i of unit u, and the unit's place in it
+    __device__ __forceinline__ void find(long long u, int &i, int &at) const {
         const int nt = row_tiles();
         int k = tiles_of(0), done = 0;
         while (done < nt) {
             const int c = min(nt, max(done, upto(k)));
-            const long long here = (long long)k * (c - done);
+            const long long here = (long long)(k + OV) * (c - done);
             if (u < here) {
-                i = done + (int)(u / k);
-                j = (int)(u % k);
+                // (a block's share of a sequence's units fits 31 bits wherever there are that many blocks)
+                const long long q = here <= 0x7fffffff ? (unsigned)u / (unsigned)(k + OV) : u / (k + OV);
+                i = done + (int)q;
+                at = (int)(u - q * (k + OV));
                 return;
             }
             u -= here;
@@ -147,7 +171,7 @@ struct Seq {
             ++k;
         }
         i = nt - 1;
-        j = 0;
+        at = 0;
     }
 };
 
@@ -156,28 +180,35 @@ struct Seq {
 template <int R>
 struct Walk {
     Seq<R> s;
-    int n, i, j0, j1, tiles;
-    long long left;
-    __device__ __forceinline__ void start(const Args &a, int n_, int i_, int j_, long long left_) {
-        n = n_; i = i_; j0 = j_; left = left_;
-        if (left > 0) { s.load(a, n); bound(); }
+    int n, i, j0, j1, tiles, at;                // at: the unit of the row tile that the range goes on with
+    long long left;                             // units of the range from there on
+    __device__ __forceinline__ void start(const Args &a, const Small &sm, long long left_) {
+        left = left_;
+        j0 = j1 = 0;
+        if (left <= 0) return;
+        n = sm.start[0]; i = sm.start[4]; at = sm.start[5];
+        s.set(a, sm.start[1], sm.start[2], sm.start[3]);
+        settle();
     }
-    __device__ __forceinline__ void bound() {
+    __device__ __forceinline__ void settle() {
         tiles = s.tiles_of(i);
-        j1 = (int)min((long long)tiles, j0 + left);
+        const int take = (int)min((long long)(tiles + OV - at), left);
+        j0 = max(0, at - OV);
+        j1 = max(0, at + take - OV);
+        if (j1 == j0) left = 0;                 // the range ends before the first key tile
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next(const Args &a) {
-        left -= j1 - j0;
+        left -= min((long long)(tiles + OV - at), left);
         if (left <= 0) return;
-        j0 = 0;
+        at = 0;
         ++i;
         while (i >= s.row_tiles()) {
             if (++n >= a.N) { left = 0; return; }
             s.load(a, n);
             i = 0;
         }
-        bound();
+        settle();
     }
 };
 
@@ -211,21 +242,50 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// Combines v[c] of the warp's 32 lanes, per column c: lane c ends up with the
-// result of column c.  Halving: 31 shuffles instead of 5 * 32.
-template <bool MAX>
-__device__ __forceinline__ float across_lanes(float (&v)[32], int lane) {
+// A 64-row accumulator (16 lanes of each sub-partition): thread l of the warp gets
+// row l % 16 of the sub-partition, columns [0, C) (l < 16) or [C, 2 C).
+__device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Combines v[c] over the 16 lanes of the half warp, per column c, by halving
+// (C - C / 16 shuffles instead of 4 C): lane l ends up with the results of
+// columns NPL l .. + NPL - 1 of all 2 C in v[0], v[1].
+template <bool MAX, int C>
+__device__ __forceinline__ void across_lanes(float (&v)[C], int lane) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        const int n = o * C / 16;
         const bool up = (lane & o) != 0;
 #pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+        for (int i = 0; i < n; ++i) {
+            const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
             const float other = __shfl_xor_sync(0xffffffffu, send, o);
             v[i] = MAX ? fmaxf(keep, other) : keep + other;
         }
     }
-    return v[0];
 }
 
 template <int R, int DV, bool PE>
@@ -233,348 +293,426 @@ __global__ void __launch_bounds__(Lay<R, DV, PE>::NT, 1)
 latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c, const Args a)
 {
     using L = Lay<R, DV, PE>;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::MISC);
-    uint64_t *empty = full + L::NS;
-    uint64_t *x_full = empty + L::NS, *x_empty = x_full + 1, *q_full = x_full + 2, *q_empty = x_full + 3;
-    uint64_t *s_full = x_full + 4;                            // [2]
-    uint64_t *p_full = x_full + 6, *o_full = x_full + 7, *drain = x_full + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_full + 9);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    long long *scan = reinterpret_cast<long long *>(x_full + 10);         // [16] warp sums, then the start
-    int *start = reinterpret_cast<int *>(scan + 16);                       // sequence, row tile, key tile
-    float *red = reinterpret_cast<float *>(start + 4);                     // [SW][32]
-    float *mine = red + L::SW * 32;                                        // [SW][2][32]: a warp's maxima and factors
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Small &z = *reinterpret_cast<Small *>(sm + L::MISC);
+    volatile int *abort_flag = &z.abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-    if (tid == 0) {
-        for (int s = 0; s < L::NS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        mbar_init(x_full, 1); mbar_init(x_empty, 1); mbar_init(q_full, 1); mbar_init(q_empty, 1);
-        mbar_init(&s_full[0], 1); mbar_init(&s_full[1], 1);
-        mbar_init(p_full, L::SW); mbar_init(o_full, 1); mbar_init(drain, 1);
-        *abort_flag = 0;
-        start[0] = 0; start[1] = 0; start[2] = 0;
-        fence_mbar_init();
+    if (smem_u32(sm) & 1023) {                  // the swizzled tiles need it; the same for every block
+        if (tid == 0) { set_device_error(a.err, kErrWaitTimeout); a.meta[2 * blockIdx.x].w = a.meta[2 * blockIdx.x + 1].w = 0; }
+        return;
     }
-    if (warp == 0) { tmem_alloc(tmem_slot, L::COLS); tmem_relinquish(); }
 
     // ---- this block's range of the (row tile, key tile) units
     const int per = (a.N + L::NT - 1) / L::NT;
     const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
     long long mysum = 0;
+    Seq<R> s0;                                  // the thread's first sequence
     for (int n = n0; n < n1; ++n) {
         Seq<R> s;
         s.load(a, n);
         if (s.bad && blockIdx.x == 0) set_device_error(a.err, paged::kErrBadPage);
+        if (n == n0) s0 = s;
         mysum += s.units();
     }
+    if (tid == 0) {
+        for (int s = 0; s < L::NS; ++s) { mbar_init(&z.full[s], 1); mbar_init(&z.empty[s], 1); }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&z.x_full[b], 1); mbar_init(&z.x_empty[b], 1);
+            mbar_init(&z.s_full[b], 1); mbar_init(&z.s_free[b], L::SW); mbar_init(&z.drain[b], 1);
+        }
+        mbar_init(&z.q_full, 1); mbar_init(&z.q_empty, 1); mbar_init(&z.p_full, L::SW); mbar_init(&z.o_full, 1);
+        z.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) { tmem_alloc(&z.tmem, L::COLS); tmem_relinquish(); }
     long long incl = mysum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) scan[warp] = incl;
+    if (lane == 31) z.scan[warp] = incl;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = z.tmem;
     long long before = incl - mysum, total = 0;
+#pragma unroll
     for (int w = 0; w < L::NT / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
+        const long long x = z.scan[w];
+        if (w < warp) before += x;
+        total += x;
     }
     // as many ranges as blocks, but none empty: the pieces of a row tile lie in consecutive blocks
-    const long long G = max(1LL, min((long long)gridDim.x, total));
-    const bool works = blockIdx.x < G && total > 0;
-    const long long u0 = works ? total * blockIdx.x / G : 0, u1 = works ? total * (blockIdx.x + 1) / G : 0;
+    const int G = total < (long long)gridDim.x ? max(1, (int)total) : (int)gridDim.x;
+    const int b = blockIdx.x;
+    long long u0 = 0, u1 = 0;                   // total * b / G, total * (b + 1) / G
+    if (b < G && total > 0) {
+        if (total <= 0x7fffffff) {
+            const unsigned q = (unsigned)total / (unsigned)G, r = (unsigned)total - q * G;
+            u0 = (long long)q * b + r * (unsigned)b / (unsigned)G;
+            u1 = (long long)q * (b + 1) + r * (unsigned)(b + 1) / (unsigned)G;
+        } else {
+            u0 = total * b / G;
+            u1 = total * (b + 1) / G;
+        }
+    }
     if (u0 < u1 && u0 >= before && u0 < before + mysum) {
         long long u = u0 - before;
-        for (int n = n0; n < n1; ++n) {
-            Seq<R> s;
-            s.load(a, n);
-            const long long here = s.units();
-            if (u < here) {
-                int i, j;
-                s.find(u, i, j);
-                start[0] = n; start[1] = i; start[2] = j;
-                break;
-            }
-            u -= here;
-        }
+        Seq<R> s = s0;
+        int n = n0;
+        for (long long here; n + 1 < n1 && u >= (here = s.units()); s.load(a, ++n)) u -= here;
+        int i, at;
+        s.find(u, i, at);
+        z.start[0] = n; z.start[1] = s.first; z.start[2] = s.L; z.start[3] = s.kv; z.start[4] = i; z.start[5] = at;
     }
     __syncthreads();
     Walk<R> w;
-    w.start(a, start[0], start[1], start[2], u1 - u0);
+    w.start(a, z, u1 - u0);
 
     if (warp == L::SW) {
         // ---------------- TMA: Q of each segment, then its key tiles ----------------
-        int st = 0, st_use = 0, tiles = 0, segs = 0;          // stage, its uses, X uses, Q uses
+        int st = 0, st_use = 0, tiles = 0, segs = 0;          // stage, its uses; key tiles and segments so far
         bool ok = true;
-        const int lps = 31 - __clz(a.page_size);
+        const int rows_box = min(a.page_size, KT);            // rows of a box
+        const int lrb = 31 - __clz(rows_box), lps = 31 - __clz(a.page_size);
+        // the page of box `lane` of key tile j (of the walk's sequence)
+        auto page_of = [&](int j, int boxes) {
+            return lane < boxes ? a.table[(long long)w.n * a.max_pages + ((j * KT + lane * rows_box) >> lps)] : 0;
+        };
+        auto boxes_of = [&](int j, int end) { return (max(0, min(KT, end - j * KT)) + rows_box - 1) >> lrb; };
         for (; w.more() && ok; w.next(a)) {
             const int end = w.s.keys_of(w.i);
-            if (lane == 0) ok = segs == 0 || wait_on(q_empty, (segs - 1) & 1, abort_flag);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
+            int boxes = boxes_of(w.j0, end);
+            int page = page_of(w.j0, boxes);
+            ok = segs == 0 || wait_on(&z.q_empty, (segs - 1) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (lane == 0) {
                 const int row = w.s.first * a.H + w.i * R;
-                mbar_arrive_expect_tx(q_full, L::NQ * L::QP);
-                for (int p = 0; p < L::NQ; ++p) tma_2d(sm + L::Q_OFF + p * L::QP, &tm_q, 64 * p, row, q_full);
+                mbar_arrive_expect_tx(&z.q_full, L::NQ * L::QP);
+                for (int p = 0; p < L::NQ; ++p) tma_2d(sm + p * L::QP, &tm_q, 64 * p, row, &z.q_full);
             }
             ++segs;
             for (int j = w.j0; j < w.j1 && ok; ++j) {
-                const int pages = (max(0, min(KT, end - j * KT)) + a.page_size - 1) >> lps;
-                int page = 0;
-                if (lane < pages) page = a.table[(long long)w.n * a.max_pages + ((j * KT) >> lps) + lane];
-                // boxes of 64 channels x one page's rows
-                for (int m = 0; m <= L::MT && ok; ++m) {
-                    const bool x = m == L::MT;
-                    if (x && !PE) break;
-                    uint64_t *fb = x ? x_full : &full[st];
-                    if (lane == 0) ok = x ? tiles == 0 || wait_on(x_empty, (tiles - 1) & 1, abort_flag)
-                                          : st_use == 0 || wait_on(&empty[st], (st_use - 1) & 1, abort_flag);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)pages * a.page_size * 128 * (x ? 1 : 2));
+                // boxes of 64 channels x (part of) one page's rows
+                const int y = (j * KT + lane * rows_box) & (a.page_size - 1);
+                const uint32_t bytes = (uint32_t)boxes * rows_box * 128;
+                if (PE) {
+                    uint64_t *fb = &z.x_full[tiles & 1];
+                    ok = tiles < 2 || wait_on(&z.x_empty[tiles & 1], ((tiles >> 1) - 1) & 1, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
                     __syncwarp();
-                    unsigned char *dst = sm + (x ? L::X_OFF : L::ST_OFF + st * L::STAGE) + lane * a.page_size * 128;
-                    if (lane < pages) {
-                        prep::tma_load_3d(dst, &tm_c, 128 * m, 0, page, fb);
-                        if (!x) prep::tma_load_3d(dst + 16384, &tm_c, 128 * m + 64, 0, page, fb);
+                    if (lane < boxes)
+                        prep::tma_load_3d(sm + L::X_OFF + (tiles & 1) * L::HALF + lane * rows_box * 128, &tm_c, DV, y, page, fb);
+                }
+                for (int m = 0; m < L::MT; ++m) {
+                    uint64_t *fb = &z.full[st];
+                    ok = st_use == 0 || wait_on(&z.empty[st], (st_use - 1) & 1, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(fb, 2 * bytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        unsigned char *dst = sm + L::ST_OFF + st * L::STAGE + lane * rows_box * 128;
+                        prep::tma_load_3d(dst, &tm_c, 128 * m, y, page, fb);
+                        prep::tma_load_3d(dst + L::HALF, &tm_c, 128 * m + 64, y, page, fb);
                     }
-                    if (!x && ++st == L::NS) { st = 0; ++st_use; }
+                    if (++st == L::NS) { st = 0; ++st_use; }
                 }
                 ++tiles;
+                if (j + 1 < w.j1) { boxes = boxes_of(j + 1, end); page = page_of(j + 1, boxes); }
             }
         }
-        if (!ok && lane == 0) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; }
-        // never leave with copies in flight into this block's shared memory
-        __syncwarp();
-        if (lane == 0 && !ok) {
-            for (int s = 0; s < L::NS; ++s) {
-                const int uses = st_use + (s < st ? 1 : 0);
-                if (uses > 0) mbar_wait(&full[s], (uses - 1) & 1, 1u << 20);
+        if (!ok) {
+            if (lane == 0) {
+                set_device_error(a.err, kErrWaitTimeout);
+                *abort_flag = 1;
+                // never leave with copies in flight into this block's shared memory
+                for (int s = 0; s < L::NS; ++s) {
+                    const int uses = st_use + (s < st ? 1 : 0);
+                    if (uses > 0) mbar_wait(&z.full[s], (uses - 1) & 1, 1u << 20);
+                }
+                for (int x = 0; PE && x < 2; ++x) {
+                    // (the last tile may have its positional piece only)
+                    const int uses = (tiles + 1 - x + 1) / 2;
+                    if (uses > 0) mbar_wait(&z.x_full[x], (uses - 1) & 1, 1u << 18);
+                    if (uses > 1) mbar_wait(&z.x_full[x], (uses - 2) & 1, 1u << 18);
+                }
+                if (segs > 0) mbar_wait(&z.q_full, (segs - 1) & 1, 1u << 20);
             }
-            if (PE && tiles > 0) mbar_wait(x_full, (tiles - 1) & 1, 1u << 20);
-            if (segs > 0) mbar_wait(q_full, (segs - 1) & 1, 1u << 20);
         }
     } else if (warp == L::SW + 1) {
-        // ---------------- MMA issuer ----------------
+        // ---------------- S^T = C Q^T ----------------
         if (lane == 0) {
-            constexpr uint32_t ID_S = idesc(128, R, false), ID_O = idesc(128, R, true);
+            constexpr uint32_t ID = idesc(64, R, false);
             const uint32_t base = smem_u32(sm);
-            const DescParts q_d = smem_desc_parts(base + L::Q_OFF, 16, 1024, 2);
+            const DescParts q_d = smem_desc_parts(base, 16, 1024, 2);
             const DescParts k_d = smem_desc_parts(base + L::ST_OFF, 16, 1024, 2);        // keys, K-major
             const DescParts x_d = smem_desc_parts(base + L::X_OFF, 16, 1024, 2);
-            const DescParts v_d = smem_desc_parts(base + L::ST_OFF, 16384, 1024, 2);     // values, MN-major
-            const DescParts p_d = smem_desc_parts(base + L::P_OFF, L::B_SBO, L::B_SBO, L::B_LAYOUT);
-            constexpr uint32_t PK = (2 * L::B_SBO) >> 4;
             int st = 0, st_use = 0, tiles = 0, segs = 0;
-            bool ok = true, any = false;
+            bool ok = true;
             for (; w.more() && ok; w.next(a)) {
-                ok = wait_on(q_full, segs & 1, abort_flag);
+                ok = wait_on(&z.q_full, segs & 1, abort_flag);
                 ++segs;
                 for (int j = w.j0; j < w.j1 && ok; ++j) {
-                    const uint32_t d = tmem + (tiles & 1) * R;
-                    int s = st, use = st_use;
-                    for (int m = 0; m < L::MT && ok; ++m) {
-                        if (!(ok = wait_on(&full[s], use & 1, abort_flag))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16_p(d, k_d.lo + ((s * L::STAGE + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4), k_d.hi,
-                                        q_d.lo + (((2 * m + (kk >> 2)) * L::QP + (kk & 3) * 32) >> 4), q_d.hi, ID_S, m > 0 || kk > 0);
-                        any = true;
-                        if (++s == L::NS) { s = 0; ++use; }
-                    }
-                    if (PE && ok && (ok = wait_on(x_full, tiles & 1, abort_flag))) {
+                    const int b2 = tiles & 1;
+                    const uint32_t d = tmem + ((uint32_t)(16 * b2) << 16);
+                    if (tiles >= 2 && !(ok = wait_on(&z.s_free[b2], ((tiles >> 1) - 1) & 1, abort_flag))) break;
+                    if (PE) {
+                        if (!(ok = wait_on(&z.x_full[b2], (tiles >> 1) & 1, abort_flag))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16_p(d, x_d.lo + ((kk * 32) >> 4), x_d.hi, q_d.lo + (((L::NQ - 1) * L::QP + kk * 32) >> 4),
-                                        q_d.hi, ID_S, 1);
-                        if (!L::ALIAS) umma_commit(x_empty);
+                            umma_bf16_p(d, x_d.lo + ((b2 * L::HALF + kk * 32) >> 4), x_d.hi,
+                                        q_d.lo + (((L::NQ - 1) * L::QP + kk * 32) >> 4), q_d.hi, ID, kk > 0);
+                        umma_commit(&z.x_empty[b2]);
                     }
-                    if (!ok) break;
-                    umma_commit(&s_full[tiles & 1]);
-                    if (j + 1 == w.j1) umma_commit(q_empty);
-                    if (!(ok = wait_on(p_full, tiles & 1, abort_flag))) break;
-                    tc_fence_after();
                     for (int m = 0; m < L::MT; ++m) {
+                        if (!(ok = wait_on(&z.full[st], st_use & 1, abort_flag))) break;
+                        tc_fence_after();
+                        const uint32_t k_lo = k_d.lo + (st * L::STAGE >> 4), q_lo = q_d.lo + (2 * m * L::QP >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16_p(tmem + L::O_COL + m * R, v_d.lo + ((st * L::STAGE + kk * 2048) >> 4), v_d.hi,
-                                        p_d.lo + kk * PK, p_d.hi, ID_O, j > w.j0 || kk > 0);
-                        umma_commit(&empty[st]);
+                            umma_bf16_p(d, k_lo + (((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4), k_d.hi,
+                                        q_lo + (((kk >> 2) * L::QP + (kk & 3) * 32) >> 4), q_d.hi, ID, PE || m > 0 || kk > 0);
                         if (++st == L::NS) { st = 0; ++st_use; }
                     }
-                    if (PE && L::ALIAS) umma_commit(x_empty);
-                    if (j + 1 == w.j1) umma_commit(o_full);
+                    if (!ok) break;
+                    umma_commit(&z.s_full[b2]);
+                    if (j + 1 == w.j1) umma_commit(&z.q_empty);
                     ++tiles;
                 }
             }
             if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; }
             // never free TMEM or shared memory under a running MMA
-            if (any) {
-                umma_commit(drain);
-                mbar_wait(drain, 0, 1u << 20);
-            }
+            umma_commit(&z.drain[0]);
+            mbar_wait(&z.drain[0], 0, 1u << 20);
+        }
+    } else if (warp == L::SW + 2) {
+        // ---------------- O^T += C^T P^T ----------------
+        if (lane == 0) {
+            constexpr uint32_t ID = idesc(128, R, true);
+            const uint32_t base = smem_u32(sm);
+            const DescParts v_d = smem_desc_parts(base + L::ST_OFF, L::HALF, 1024, 2);   // values, MN-major
+            const DescParts p_d = smem_desc_parts(base + L::P_OFF, L::B_SBO, L::B_SBO, L::B_LAYOUT);
+            constexpr uint32_t PK = (2 * L::B_SBO) >> 4;
+            int st = 0, tiles = 0;
+            bool ok = true;
+            for (; w.more() && ok; w.next(a))
+                for (int j = w.j0; j < w.j1; ++j) {
+                    if (!(ok = wait_on(&z.p_full, tiles & 1, abort_flag))) break;
+                    tc_fence_after();
+                    for (int m = 0; m < L::MT; ++m) {
+                        const uint32_t v_lo = v_d.lo + (st * L::STAGE >> 4), d = tmem + L::O_COL + m * R;
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            umma_bf16_p(d, v_lo + ((kk * 2048) >> 4), v_d.hi, p_d.lo + kk * PK, p_d.hi, ID, j > w.j0 || kk > 0);
+                        umma_commit(&z.empty[st]);
+                        if (++st == L::NS) st = 0;
+                    }
+                    umma_commit(&z.o_full);
+                    ++tiles;
+                }
+            if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; }
+            umma_commit(&z.drain[1]);
+            mbar_wait(&z.drain[1], 0, 1u << 20);
         }
     } else {
-        // ---------------- softmax and output: thread = key t of the tile (TMEM lane),
-        // rows 32 cg .. 32 cg + 31 of the row tile ----------------
-        const int t = 32 * (warp & 3) + lane, cg = warp >> 2;
-        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 32 * cg;
-        float *my_m = mine + warp * 64, *my_f = my_m + 32;
-        float *my_red = red + cg * 128;
-        int tiles = 0, segs = 0;
+        // ---------------- softmax and output: key r of the tile, rows C half .. + C - 1 of
+        // the row tile; the statistics of rows NPL lane .. in every warp alike ----------------
+        constexpr int C = L::C, NPL = L::NPL;
+        const int t = 32 * warp + lane, half = lane >> 4, r = 16 * warp + (lane & 15);
+        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        float *mine = z.mine[warp];
+        const float *mine_c = mine + C * half;
+        int tiles = 0;
         bool ok = true;
-        int4 meta = make_int4(0, 0, 0, 0);
-        for (; w.more() && ok; w.next(a)) {
+        int4 meta[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+        long long at0 = u0;                                              // units of the range before the segment
+        for (; w.more() && ok;) {
             const int rows = min(R, w.s.rows() - w.i * R);               // of this row tile
             const int end = w.s.keys_of(w.i);
-            const int row = 32 * cg + lane;                              // this lane's row, for the statistics
-            const int sees = row < rows ? w.s.sees(w.i * R + row) : 0;
-            const int least = __reduce_min_sync(0xffffffffu, row < rows ? sees : 0x7fffffff);
+            int sees[NPL], least = 0x7fffffff;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int row = NPL * lane + i;
+                sees[i] = row < rows ? w.s.sees(w.i * R + row) : 0;
+                if (row < rows) least = min(least, sees[i]);
+            }
+            least = __reduce_min_sync(0xffffffffu, least);
             // the sequence's pages, all of them: every block that has a piece of it comes to the same answer
             bool bad = false;
-            for (int p = t; p * a.page_size < w.s.kv; p += 128) {
+            for (int p = t; (long long)p * a.page_size < w.s.kv; p += 128) {
                 const int pg = a.table[(long long)w.n * a.max_pages + p];
                 bad |= pg < 0 || pg >= a.num_pages;
             }
-            float m_run = -INFINITY, l[32];
+            float m_run[NPL], l[C];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) l[c] = 0.f;
+            for (int i = 0; i < NPL; ++i) m_run[i] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < C; ++c) l[c] = 0.f;
             for (int j = w.j0; j < w.j1; ++j) {
-                ok = wait_on(&s_full[tiles & 1], (tiles >> 1) & 1, abort_flag);
+                ok = ok && wait_on(&z.s_full[tiles & 1], (tiles >> 1) & 1, abort_flag);
                 tc_fence_after();
-                float x[32], y[32];
-                tmem_ld32(lanes + (tiles & 1) * R, x);
+                float x[C], y[C];
+                tmem_ld_half(lanes + ((uint32_t)(16 * (tiles & 1)) << 16), x);
                 tmem_wait_ld();
-                const int key = j * KT + t;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&z.s_free[tiles & 1]);
+                const int key = j * KT + r;
                 if (j * KT + KT > least) {
-                    // some row of this group does not see the whole tile
-                    my_m[lane] = __int_as_float(sees);
+                    // some row does not see the whole tile
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i) mine[NPL * lane + i] = __int_as_float(sees[i]);
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] = key < __float_as_int(my_m[c]) ? x[c] * a.sl2 : -INFINITY;
+                    for (int c = 0; c < C; ++c) x[c] = key < __float_as_int(mine_c[c]) ? x[c] * a.sl2 : -INFINITY;
                     __syncwarp();
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] *= a.sl2;
+                    for (int c = 0; c < C; ++c) x[c] *= a.sl2;
                 }
 #pragma unroll
-                for (int c = 0; c < 32; ++c) y[c] = x[c];
-                my_red[(warp & 3) * 32 + lane] = across_lanes<true>(y, lane);
-                if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
-                const float mt = fmaxf(fmaxf(my_red[lane], my_red[32 + lane]), fmaxf(my_red[64 + lane], my_red[96 + lane]));
-                // the reference is raised only when the maximum has outgrown it by 2^TH
-                const bool raise = mt > m_run + TH || (m_run == -INFINITY && mt > -INFINITY);
-                const float m_new = raise ? mt : m_run;
-                my_m[lane] = m_new == -INFINITY ? 0.f : m_new;
-                my_f[lane] = raise ? exp2f(m_run - m_new) : 1.f;
-                m_run = m_new;
-                const bool any = __any_sync(0xffffffffu, raise) && j > w.j0;
+                for (int c = 0; c < C; ++c) y[c] = x[c];
+                across_lanes<true, C>(y, lane);
+                // every warp is done with the previous tile's maxima
+                if (tiles > 0 && !wait_on(&z.p_full, (tiles - 1) & 1, abort_flag)) ok = false;
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) z.red[warp][NPL * lane + i] = y[i];
+                if (named_bar_or(1, 128, !ok)) { ok = false; break; }
+                bool any = false;
+                float f[NPL];
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    const int row = NPL * lane + i;
+                    const float mt = fmaxf(fmaxf(z.red[0][row], z.red[1][row]), fmaxf(z.red[2][row], z.red[3][row]));
+                    // the reference is raised only when the maximum has outgrown it by 2^TH
+                    const bool raise = mt > m_run[i] + TH || (m_run[i] == -INFINITY && mt > -INFINITY);
+                    f[i] = raise ? exp2f(m_run[i] - mt) : 1.f;
+                    if (raise) m_run[i] = mt;
+                    any |= raise;
+                    mine[row] = m_run[i] == -INFINITY ? 0.f : m_run[i];
+                }
+                any = __any_sync(0xffffffffu, any) && j > w.j0;
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = prep::ex2_approx(x[c] - my_m[c]);
+                for (int c = 0; c < C; ++c) x[c] = prep::ex2_approx(x[c] - mine_c[c]);
+                // P^T and O^T are free once the previous tile's product is done
+                if (tiles > 0 && !wait_on(&z.o_full, (tiles - 1) & 1, abort_flag)) ok = false;
+                tc_fence_after();
                 if (any) {
-                    // the product of the previous tile is complete: S^T of this one was issued after it
+                    __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) l[c] *= my_f[c];
-                    for (int m = 0; m < L::MT; ++m) {
-                        tmem_ld32(lanes + L::O_COL + m * R, y);
+                    for (int i = 0; i < NPL; ++i) mine[NPL * lane + i] = f[i];
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < C; ++c) l[c] *= mine_c[c];
+                    for (int m = 0; m < L::MT * NPL; ++m) {
+                        float o[32];
+                        tmem_ld32(lanes + L::O_COL + m * 32, o);
                         tmem_wait_ld();
+                        const float *fm = mine + 32 * (m % NPL);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) y[c] *= my_f[c];
-                        tmem_st32(lanes + L::O_COL + m * R, y);
+                        for (int c = 0; c < 32; ++c) o[c] *= fm[c];
+                        tmem_st32(lanes + L::O_COL + m * 32, o);
                     }
                     tmem_wait_st();
                 }
                 unsigned char *P = sm + L::P_OFF;
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *reinterpret_cast<uint4 *>(P + L::p_off(t, 4 * cg + g)) =
+                for (int g = 0; g < C / 8; ++g)
+                    *reinterpret_cast<uint4 *>(P + L::p_off(r, C / 8 * half + g)) =
                         make_uint4(pack_bf16(x[8 * g], x[8 * g + 1]), pack_bf16(x[8 * g + 2], x[8 * g + 3]),
                                    pack_bf16(x[8 * g + 4], x[8 * g + 5]), pack_bf16(x[8 * g + 6], x[8 * g + 7]));
 #pragma unroll
-                for (int c = 0; c < 32; ++c) l[c] += x[c];
-                if (key >= end && cg == 0) {
+                for (int c = 0; c < C; ++c) l[c] += x[c];
+                if (key >= end) {
                     // rows that hold no key of this row tile may hold anything: 0 * NaN is not 0
                     int s = (int)((long long)tiles * L::MT % L::NS);
                     for (int m = 0; m < L::MT; ++m) {
-                        unsigned char *v = sm + L::ST_OFF + s * L::STAGE + t * 128;
+                        unsigned char *v = sm + L::ST_OFF + s * L::STAGE + half * L::HALF + r * 128;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            *reinterpret_cast<uint4 *>(v + 16 * e) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(v + 16384 + 16 * e) = make_uint4(0, 0, 0, 0);
-                        }
+                        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(v + 16 * e) = make_uint4(0, 0, 0, 0);
                         if (++s == L::NS) s = 0;
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
+                if (lane == 0) mbar_arrive(&z.p_full);
                 ++tiles;
             }
             if (!ok) break;
-            ok = wait_on(o_full, segs & 1, abort_flag);
-            ++segs;
+            ok = wait_on(&z.o_full, (tiles - 1) & 1, abort_flag);
             tc_fence_after();
-            my_red[(warp & 3) * 32 + lane] = across_lanes<false>(l, lane);
-            if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
-            const float sum = (my_red[lane] + my_red[32 + lane]) + (my_red[64 + lane] + my_red[96 + lane]);
-            bad = named_bar_or(1 + cg, 128, bad);
+            across_lanes<false, C>(l, lane);
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) z.red[warp][NPL * lane + i] = l[i];
+            if (named_bar_or(1, 128, !ok)) { ok = false; break; }
+            float sum[NPL];
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int row = NPL * lane + i;
+                sum[i] = (z.red[0][row] + z.red[1][row]) + (z.red[2][row] + z.red[3][row]);
+            }
+            bad = named_bar_or(1, 128, bad);
             if (bad && tid == 0) set_device_error(a.err, paged::kErrBadPage);
             const long long row0 = (long long)w.s.first * a.H + (long long)w.i * R;
             if (w.j0 == 0 && w.j1 == w.tiles) {
                 // the whole row tile was here
-                my_m[lane] = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) {
+                    const int row = NPL * lane + i;
+                    mine[row] = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
+                    if (a.lse && warp == 0 && row < rows && !bad)
+                        a.lse[row0 + row] = sum[i] > 0.f ? (m_run[i] + log2f(sum[i])) * 0.693147180559945f : -INFINITY;
+                }
                 __syncwarp();
-                if (!bad) {
-                    if (a.lse && (warp & 3) == 0 && row < rows)
-                        a.lse[row0 + row] = sum > 0.f ? (m_run + log2f(sum)) * 0.693147180559945f : -INFINITY;
-                    for (int m = 0; m < L::MT; ++m) {
+                if (!bad)
+                    for (int m = 0; m < L::MT * NPL; ++m) {
                         float o[32];
-                        tmem_ld32(lanes + L::O_COL + m * R, o);
+                        tmem_ld32(lanes + L::O_COL + m * 32, o);
                         tmem_wait_ld();
+                        const int c0 = 32 * (m % NPL), ch = 128 * (m / NPL) + t;
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (32 * cg + c < rows)
-                                a.out[(row0 + 32 * cg + c) * DV + 128 * m + t] = __float2bfloat16_rn(o[c] * my_m[c]);
+                            if (c0 + c < rows)
+                                a.out[(row0 + c0 + c) * DV + ch] = __float2bfloat16_rn(o[c] * mine[c0 + c]);
                     }
-                }
             } else {
                 // a piece: slot 0 if it continues the row tile, slot 1 if it begins it
-                const int slot = 2 * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-                if ((warp & 3) == 0) {
-                    float *ml = a.ws_ml + ((size_t)slot * R + row) * 2;
-                    ml[0] = m_run;
-                    ml[1] = bad ? -1.f : sum;
-                }
-                for (int m = 0; m < L::MT; ++m) {
-                    float o[32];
-                    tmem_ld32(lanes + L::O_COL + m * R, o);
-                    tmem_wait_ld();
+                const int slot = 2 * b + (w.j0 == 0 ? 1 : 0);
+                if (warp == 0)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        a.ws_o[((size_t)slot * R + 32 * cg + c) * DV + 128 * m + t] = o[c];
+                    for (int i = 0; i < NPL; ++i) {
+                        float *ml = a.ws_ml + ((size_t)slot * R + NPL * lane + i) * 2;
+                        ml[0] = m_run[i];
+                        ml[1] = bad ? -1.f : sum[i];
+                    }
+                for (int m = 0; m < L::MT * NPL; ++m) {
+                    float o[32];
+                    tmem_ld32(lanes + L::O_COL + m * 32, o);
+                    tmem_wait_ld();
+                    float *dst = a.ws_o + ((size_t)slot * R + 32 * (m % NPL)) * DV + 128 * (m / NPL) + t;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) dst[(size_t)c * DV] = o[c];
                 }
-                if (w.j0 == 0) {
-                    // its last unit lies in block b: u0(b) <= last < u0(b + 1)
-                    const long long last = u1 - 1 + (w.tiles - w.j1);
-                    long long b = ((last + 1) * G + total - 1) / total - 1;
-                    meta = make_int4((int)row0, rows, (int)(b - blockIdx.x), 0);
+                if (tid == 0) {
+                    // the blocks of its first and last key tile; unit u is in block (u G + G - 1) / total
+                    const long long first = at0 - w.at + OV, last = first + w.tiles - 1;
+                    auto block_of = [&](long long u) { return (int)((u * G + G - 1) / total); };
+                    const int b0 = w.j0 == 0 ? b : block_of(first);
+                    meta[w.j0 == 0 ? 1 : 0] = make_int4((int)row0, rows, b0, block_of(last) - b0 + 1);
                 }
             }
             tc_fence_before();
             __syncwarp();
+            at0 += w.tiles + OV - w.at;                                  // (of no use after the last segment)
+            w.next(a);
         }
-        if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; meta.z = 0; }
-        if (tid == 0) a.meta[blockIdx.x] = meta;
+        if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; meta[0].w = meta[1].w = 0; }
+        if (tid == 0) { a.meta[2 * b] = meta[0]; a.meta[2 * b + 1] = meta[1]; }
     }
     __syncwarp();
     tc_fence_before();
@@ -583,62 +721,85 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == 0) tmem_dealloc(tmem, L::COLS);
 }
 
-// Joins the pieces of a row tile that begins in block x's range and goes on in
-// the next ones: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.  One row
-// a block; the pieces are shared out over four groups of threads.
+// Joins the pieces of the row tiles that were split: with M = max m_k,
+//     out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,   lse from M and the sum.
+// The rows of a split tile are shared out over the blocks whose ranges it lies
+// in (block x has up to two such tiles: one that it continues, one that it
+// begins), and over gridDim.y.  With few pieces a warp takes a row; with many
+// the block's warps share a row's pieces and add their parts up in order.
+constexpr int CW = 8;                          // warps
+constexpr int FEW = 8;                         // pieces that one warp takes
+
 template <int R, int DV>
-__global__ void __launch_bounds__(DV)
+__global__ void __launch_bounds__(32 * CW)
 latent_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_ml, const int4 *__restrict__ meta,
                       __nv_bfloat16 *__restrict__ out, float *__restrict__ lse)
 {
-    const int b = blockIdx.x, r = blockIdx.y;
-    const int4 mt = meta[b];
-    if (mt.z == 0 || r >= mt.y) return;
-    const int pieces = mt.z + 1;
-    auto slot = [&](int k) { return k == 0 ? 2 * b + 1 : 2 * (b + k); };
-    __shared__ float4 part[4][DV / 4];
-    __shared__ float red[DV / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float M = -INFINITY;
-    bool bad = false;
-    for (int k = tid; k < pieces; k += DV) {
-        const float2 x = *reinterpret_cast<const float2 *>(ws_ml + ((size_t)slot(k) * R + r) * 2);
-        M = fmaxf(M, x.x);
-        bad |= x.y < 0.f;
-    }
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[warp] = M;
-    if (__syncthreads_or(bad)) return;
-    for (int i = 0; i < DV / 32; ++i) M = fmaxf(M, red[i]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    const int g = tid / (DV / 4), c = tid % (DV / 4);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int k = g; k < pieces; k += 4) {
-        const size_t at = (size_t)slot(k) * R + r;
-        const float2 x = *reinterpret_cast<const float2 *>(ws_ml + at * 2);
-        const float f = exp2f(x.x - ref);
-        const float4 o = *reinterpret_cast<const float4 *>(ws_o + at * DV + 4 * c);
-        acc.x = fmaf(f, o.x, acc.x); acc.y = fmaf(f, o.y, acc.y);
-        acc.z = fmaf(f, o.z, acc.z); acc.w = fmaf(f, o.w, acc.w);
-        l = fmaf(f, x.y, l);
-    }
-    part[g][c] = acc;
-    __syncthreads();                    // (red was read above: every thread is past it)
-    if (c == 0) red[g] = l;
-    __syncthreads();
-    if (g == 0) {
-        l = (red[0] + red[1]) + (red[2] + red[3]);
-        float4 s = part[0][c];
-        for (int k = 1; k < 4; ++k) {
-            s.x += part[k][c].x; s.y += part[k][c].y; s.z += part[k][c].z; s.w += part[k][c].w;
+    constexpr int V = DV / 128;                // float4's of a lane
+    __shared__ float4 part[CW][DV / 4];
+    __shared__ float part_l[CW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int e = 0; e < 2; ++e) {
+        const int4 mt = meta[2 * blockIdx.x + e];
+        if (mt.w == 0) continue;
+        const int pieces = mt.w, k0 = blockIdx.x - mt.z;
+        const bool few = pieces <= FEW;
+        auto at = [&](int k, int r) { return (size_t)(k == 0 ? 2 * mt.z + 1 : 2 * (mt.z + k)) * R + r; };
+        // rows k0, k0 + pieces, ...
+        const int step = pieces * gridDim.y * (few ? CW : 1);
+        for (int r = k0 + pieces * (blockIdx.y * (few ? CW : 1) + (few ? warp : 0)); r < mt.y; r += step) {
+            float M = -INFINITY;
+            bool bad = false;
+            for (int k = lane; k < pieces; k += 32) {
+                const float2 x = *reinterpret_cast<const float2 *>(ws_ml + at(k, r) * 2);
+                M = fmaxf(M, x.x);
+                bad |= x.y < 0.f;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            if (__any_sync(0xffffffffu, bad)) continue;                  // (the same in all warps)
+            const float ref = M == -INFINITY ? 0.f : M;
+            float4 acc[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll 2
+            for (int k = few ? 0 : warp; k < pieces; k += few ? 1 : CW) {
+                const float2 x = *reinterpret_cast<const float2 *>(ws_ml + at(k, r) * 2);
+                const float f = exp2f(x.x - ref);
+                const float4 *o = reinterpret_cast<const float4 *>(ws_o + at(k, r) * DV) + lane;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float4 y = o[32 * v];
+                    acc[v].x = fmaf(f, y.x, acc[v].x); acc[v].y = fmaf(f, y.y, acc[v].y);
+                    acc[v].z = fmaf(f, y.z, acc[v].z); acc[v].w = fmaf(f, y.w, acc[v].w);
+                }
+                l = fmaf(f, x.y, l);
+            }
+            if (!few) {
+                __syncthreads();
+#pragma unroll
+                for (int v = 0; v < V; ++v) part[warp][32 * v + lane] = acc[v];
+                if (lane == 0) part_l[warp] = l;
+                __syncthreads();
+                if (warp != 0) continue;
+                for (int k = 1; k < CW; ++k) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float4 y = part[k][32 * v + lane];
+                        acc[v].x += y.x; acc[v].y += y.y; acc[v].z += y.z; acc[v].w += y.w;
+                    }
+                    l += part_l[k];
+                }
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const size_t row = (size_t)mt.x + r;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                reinterpret_cast<uint2 *>(out + row * DV)[32 * v + lane] =
+                    make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv), pack_bf16(acc[v].z * inv, acc[v].w * inv));
+            if (lane == 0 && lse) lse[row] = l > 0.f ? (M + log2f(l)) * 0.693147180559945f : -INFINITY;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const size_t row = (size_t)mt.x + r;
-        *reinterpret_cast<uint2 *>(out + row * DV + 4 * c) =
-            make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
-        if (c == 0 && lse) lse[row] = l > 0.f ? (M + log2f(l)) * 0.693147180559945f : -INFINITY;
     }
 }
 
@@ -653,7 +814,7 @@ cudaError_t make_maps(CUtensorMap *q, CUtensorMap *c, const void *qp, const void
         return cudaErrorInvalidValue;
     const cuuint64_t cd[3] = {(cuuint64_t)dk, (cuuint64_t)p.page_size, (cuuint64_t)p.num_pages};
     const cuuint64_t cs[2] = {(cuuint64_t)dk * 2, (cuuint64_t)p.page_stride * 2};
-    const cuuint32_t cb[3] = {64, (cuuint32_t)p.page_size, 1};
+    const cuuint32_t cb[3] = {64, (cuuint32_t)(p.page_size < KT ? p.page_size : KT), 1};
     if (fn(c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(cp), cd, cs, cb, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
@@ -665,8 +826,7 @@ cudaError_t launch_t(const void *q, const void *cache, const PagedPlan &p, void 
                      void *ws, int sms, int *err, cudaStream_t st)
 {
     using L = Lay<R, DV, PE>;
-    static_assert(L::NS >= L::MT, "a key tile must fit the ring");
-    static_assert((2 * L::NS + 20) * 8 + 128 + 16 + (L::SW * 32 + L::SW * 64) * 4 + 64 <= 4096, "small tables");
+    static_assert(L::NS >= L::MT && L::NS <= 12, "a key tile must fit the ring");
     CUtensorMap mq, mc;
     cudaError_t e = make_maps(&mq, &mc, q, cache, p, DV + (PE ? 64 : 0), R);
     if (e != cudaSuccess) return e;
@@ -682,12 +842,12 @@ cudaError_t launch_t(const void *q, const void *cache, const PagedPlan &p, void 
     a.sl2 = scale * 1.44269504088896f;
     a.full = full;
     a.err = err;
-    const size_t smem = L::BYTES + 1024;
+    const size_t smem = L::MISC + L::SMALL;
     e = cudaFuncSetAttribute(latent_attn_kernel<R, DV, PE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     latent_attn_kernel<R, DV, PE><<<sms, L::NT, smem, st>>>(mq, mc, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    latent_combine_kernel<R, DV><<<dim3(sms, R), DV, 0, st>>>(a.ws_o, a.ws_ml, a.meta, a.out, lse);
+    latent_combine_kernel<R, DV><<<dim3(sms, 4), 32 * CW, 0, st>>>(a.ws_o, a.ws_ml, a.meta, a.out, lse);
     return cudaGetLastError();
 }
 
@@ -698,7 +858,7 @@ int rows_of_tile(const PagedPlan &p) { return (long long)p.T * p.H <= 32LL * p.N
 
 size_t latent_attn_workspace(const PagedPlan &p, int dv, int sms) {
     const size_t R = rows_of_tile(p);
-    return 2 * (size_t)sms * R * (dv + 2) * sizeof(float) + sms * sizeof(int4);
+    return 2 * (size_t)sms * (R * (dv + 2) * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t launch_latent_attn(const void *q, const void *cache, const PagedPlan &p, void *out, float *lse,
