@@ -222,6 +222,27 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile
     return false;
 }
 
+// The same for a warp with a barrier per lane (null: none), all of them polled
+// at once: a poll costs a few hundred cycles, however many barriers it asks.
+__device__ __forceinline__ bool polled(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, bar == nullptr || mbar_test_wait(bar, parity));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    if (polled(bar, parity)) return true;
+    return __all_sync(0xffffffffu, bar == nullptr || wait_on(bar, parity, abort_flag));
+}
+
+// One lane of the warp, chosen by the hardware.  The products are issued by
+// whole warps under this, with operands that come from lane 0 (uniform_of): the
+// compiler then keeps descriptors in uniform registers, as the instruction wants
+// them: 36 cycles an issue, 48 from a loop that lane 0 runs alone.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+template <typename T> __device__ __forceinline__ T uniform_of(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
@@ -443,76 +464,113 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (warp == L::SW + 1) {
         // ---------------- S^T = C Q^T ----------------
-        if (lane == 0) {
-            constexpr uint32_t ID = idesc(64, R, false);
-            const uint32_t base = smem_u32(sm);
-            const DescParts q_d = smem_desc_parts(base, 16, 1024, 2);
-            const DescParts k_d = smem_desc_parts(base + L::ST_OFF, 16, 1024, 2);        // keys, K-major
-            const DescParts x_d = smem_desc_parts(base + L::X_OFF, 16, 1024, 2);
-            int st = 0, st_use = 0, tiles = 0, segs = 0;
-            bool ok = true;
-            for (; w.more() && ok; w.next(a)) {
-                ok = wait_on(&z.q_full, segs & 1, abort_flag);
-                ++segs;
-                for (int j = w.j0; j < w.j1 && ok; ++j) {
-                    const int b2 = tiles & 1;
-                    const uint32_t d = tmem + ((uint32_t)(16 * b2) << 16);
-                    if (tiles >= 2 && !(ok = wait_on(&z.s_free[b2], ((tiles >> 1) - 1) & 1, abort_flag))) break;
-                    if (PE) {
-                        if (!(ok = wait_on(&z.x_full[b2], (tiles >> 1) & 1, abort_flag))) break;
-                        tc_fence_after();
+        constexpr uint32_t ID = idesc(64, R, false);
+        const uint32_t base = smem_u32(sm);
+        const DescParts q_d = smem_desc_parts(base, 16, 1024, 2);
+        const DescParts k_d = smem_desc_parts(base + L::ST_OFF, 16, 1024, 2);            // keys, K-major
+        const DescParts x_d = smem_desc_parts(base + L::X_OFF, 16, 1024, 2);
+        int st = 0, st_use = 0, tiles = 0, segs = 0;
+        bool ok = true;
+        for (; w.more() && ok; w.next(a)) {
+            for (int j = w.j0; j < w.j1 && ok; ++j) {
+                const int b2 = uniform_of(tiles & 1);
+                const uint32_t d = uniform_of(tmem) + ((uint32_t)(16 * b2) << 16);
+                // everything that the tile waits for, asked at once: its stages, its
+                // positional piece, a free S^T, Q
+                uint64_t *bar = nullptr;
+                uint32_t parity = 0;
+                if (lane < L::MT) {
+                    const int s = st + lane;
+                    bar = &z.full[s < L::NS ? s : s - L::NS];
+                    parity = (st_use + (s < L::NS ? 0 : 1)) & 1;
+                } else if (PE && lane == L::MT) {
+                    bar = &z.x_full[b2];
+                    parity = (tiles >> 1) & 1;
+                } else if (lane == L::MT + 1 && tiles >= 2) {
+                    bar = &z.s_free[b2];
+                    parity = ((tiles >> 1) - 1) & 1;
+                } else if (lane == L::MT + 2 && j == w.j0) {
+                    bar = &z.q_full;
+                    parity = segs & 1;
+                }
+                const bool all = polled(bar, parity);
+                // else one by one: S^T starts with what has landed
+                if (!all) ok = warp_wait(lane < L::MT ? nullptr : bar, parity, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (PE) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_bf16_p(d, x_d.lo + ((b2 * L::HALF + kk * 32) >> 4), x_d.hi,
                                         q_d.lo + (((L::NQ - 1) * L::QP + kk * 32) >> 4), q_d.hi, ID, kk > 0);
                         umma_commit(&z.x_empty[b2]);
                     }
-                    for (int m = 0; m < L::MT; ++m) {
-                        if (!(ok = wait_on(&z.full[st], st_use & 1, abort_flag))) break;
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int m = 0; m < L::MT; ++m) {
+                    if (ok && !all) {
+                        ok = __all_sync(0xffffffffu, wait_on(&z.full[st], st_use & 1, abort_flag));
                         tc_fence_after();
-                        const uint32_t k_lo = k_d.lo + (st * L::STAGE >> 4), q_lo = q_d.lo + (2 * m * L::QP >> 4);
+                    }
+                    const uint32_t k_lo = k_d.lo + (uniform_of(st) * L::STAGE >> 4), q_lo = q_d.lo + (2 * m * L::QP >> 4);
+                    if (ok && elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             umma_bf16_p(d, k_lo + (((kk >> 2) * L::HALF + (kk & 3) * 32) >> 4), k_d.hi,
                                         q_lo + (((kk >> 2) * L::QP + (kk & 3) * 32) >> 4), q_d.hi, ID, PE || m > 0 || kk > 0);
-                        if (++st == L::NS) { st = 0; ++st_use; }
                     }
-                    if (!ok) break;
+                    __syncwarp();
+                    if (++st == L::NS) { st = 0; ++st_use; }
+                }
+                if (!ok) break;
+                if (elect_one()) {
                     umma_commit(&z.s_full[b2]);
                     if (j + 1 == w.j1) umma_commit(&z.q_empty);
-                    ++tiles;
                 }
+                __syncwarp();
+                ++tiles;
             }
+            ++segs;
+        }
+        // never free TMEM or shared memory under a running MMA (the elected lane is the same each time)
+        if (elect_one()) {
             if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; }
-            // never free TMEM or shared memory under a running MMA
             umma_commit(&z.drain[0]);
             mbar_wait(&z.drain[0], 0, 1u << 20);
         }
     } else if (warp == L::SW + 2) {
         // ---------------- O^T += C^T P^T ----------------
-        if (lane == 0) {
-            constexpr uint32_t ID = idesc(128, R, true);
-            const uint32_t base = smem_u32(sm);
-            const DescParts v_d = smem_desc_parts(base + L::ST_OFF, L::HALF, 1024, 2);   // values, MN-major
-            const DescParts p_d = smem_desc_parts(base + L::P_OFF, L::B_SBO, L::B_SBO, L::B_LAYOUT);
-            constexpr uint32_t PK = (2 * L::B_SBO) >> 4;
-            int st = 0, tiles = 0;
-            bool ok = true;
-            for (; w.more() && ok; w.next(a))
-                for (int j = w.j0; j < w.j1; ++j) {
-                    if (!(ok = wait_on(&z.p_full, tiles & 1, abort_flag))) break;
-                    tc_fence_after();
-                    for (int m = 0; m < L::MT; ++m) {
-                        const uint32_t v_lo = v_d.lo + (st * L::STAGE >> 4), d = tmem + L::O_COL + m * R;
+        constexpr uint32_t ID = idesc(128, R, true);
+        const uint32_t base = smem_u32(sm);
+        const DescParts v_d = smem_desc_parts(base + L::ST_OFF, L::HALF, 1024, 2);       // values, MN-major
+        const DescParts p_d = smem_desc_parts(base + L::P_OFF, L::B_SBO, L::B_SBO, L::B_LAYOUT);
+        constexpr uint32_t PK = (2 * L::B_SBO) >> 4;
+        int st = 0, tiles = 0;
+        bool ok = true;
+        for (; w.more() && ok; w.next(a))
+            for (int j = w.j0; j < w.j1; ++j) {
+                if (!(ok = __all_sync(0xffffffffu, wait_on(&z.p_full, tiles & 1, abort_flag)))) break;
+                tc_fence_after();
+                const uint32_t o = uniform_of(tmem) + L::O_COL, more = uniform_of((int)(j > w.j0));
+#pragma unroll
+                for (int m = 0; m < L::MT; ++m) {
+                    const int s = uniform_of(st);
+                    const uint32_t v_lo = v_d.lo + (s * L::STAGE >> 4);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk)
-                            umma_bf16_p(d, v_lo + ((kk * 2048) >> 4), v_d.hi, p_d.lo + kk * PK, p_d.hi, ID, j > w.j0 || kk > 0);
-                        umma_commit(&z.empty[st]);
-                        if (++st == L::NS) st = 0;
+                            umma_bf16_p(o + m * R, v_lo + ((kk * 2048) >> 4), v_d.hi, p_d.lo + kk * PK, p_d.hi, ID, kk > 0 ? 1 : more);
+                        umma_commit(&z.empty[s]);
+                        if (m + 1 == L::MT) umma_commit(&z.o_full);
                     }
-                    umma_commit(&z.o_full);
-                    ++tiles;
+                    __syncwarp();
+                    if (++st == L::NS) st = 0;
                 }
+                ++tiles;
+            }
+        if (elect_one()) {
             if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; }
             umma_commit(&z.drain[1]);
             mbar_wait(&z.drain[1], 0, 1u << 20);
@@ -552,7 +610,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int c = 0; c < C; ++c) l[c] = 0.f;
             for (int j = w.j0; j < w.j1; ++j) {
-                ok = ok && wait_on(&z.s_full[tiles & 1], (tiles >> 1) & 1, abort_flag);
+                // S^T of this tile is there; O^T, P^T and the maxima of the previous one are done with
+                uint64_t *bar = lane == 0 ? &z.s_full[tiles & 1] : lane == 1 && tiles > 0 ? &z.o_full : nullptr;
+                ok = ok && warp_wait(bar, lane == 0 ? (tiles >> 1) & 1 : (tiles - 1) & 1, abort_flag);
                 tc_fence_after();
                 float x[C], y[C];
                 tmem_ld_half(lanes + ((uint32_t)(16 * (tiles & 1)) << 16), x);
@@ -576,8 +636,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int c = 0; c < C; ++c) y[c] = x[c];
                 across_lanes<true, C>(y, lane);
-                // every warp is done with the previous tile's maxima
-                if (tiles > 0 && !wait_on(&z.p_full, (tiles - 1) & 1, abort_flag)) ok = false;
 #pragma unroll
                 for (int i = 0; i < NPL; ++i) z.red[warp][NPL * lane + i] = y[i];
                 if (named_bar_or(1, 128, !ok)) { ok = false; break; }
@@ -598,9 +656,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < C; ++c) x[c] = prep::ex2_approx(x[c] - mine_c[c]);
-                // P^T and O^T are free once the previous tile's product is done
-                if (tiles > 0 && !wait_on(&z.o_full, (tiles - 1) & 1, abort_flag)) ok = false;
-                tc_fence_after();
                 if (any) {
                     __syncwarp();
 #pragma unroll
