@@ -20,7 +20,7 @@
 // ranges go as (O, m, l) in fp32 to a workspace and latent_combine_kernel joins
 // them in a fixed order, so results do not depend on timing.
 //
-// Roles: four softmax warps (a thread has one key of S^T and half of the rows),
+// Roles: four softmax warps per 32 rows (a thread has one key of S^T and 16 rows),
 // a TMA warp, and one warp each to issue the two products, so that S^T of the
 // next tile runs while the softmax of this one does.  Every wait is bounded and
 // watches an abort flag; a wait that runs out sets the device error word and the
@@ -56,10 +56,9 @@ template <int R, int DV, bool PE>
 struct Lay {
     static constexpr int MT = DV / 128;                       // stages (128 channels) of a key tile
     static constexpr int NQ = DV / 64 + (PE ? 1 : 0);         // 64-channel pieces of Q
-    static constexpr int SW = 4;                              // softmax warps
+    static constexpr int CG = R / 32;                         // groups of 32 rows, four softmax warps each
+    static constexpr int SW = 4 * CG;
     static constexpr int NT = 32 * (SW + 3);
-    static constexpr int C = R / 2;                           // rows (columns of S^T) of a softmax thread
-    static constexpr int NPL = R / 32;                        // columns whose statistics a lane holds
     static constexpr uint32_t HALF = KT * 128;                // 64 keys x 64 channels
     static constexpr uint32_t STAGE = 2 * HALF;
     static constexpr uint32_t QP = R * 128;                   // one piece of Q
@@ -86,13 +85,13 @@ struct Lay {
 // The small tables behind the stages.
 struct Small {
     uint64_t full[12], empty[12], x_full[2], x_empty[2], q_full, q_empty, s_full[2], s_free[2], p_full, o_full, drain[2];
-    long long scan[8];
+    long long scan[12];
     long long start_u;           // first unit of the block's row tile, counted over all
     int start[6];                // sequence, its first token, new tokens, keys; row tile; unit in it
     uint32_t tmem;
     int abort_flag;
-    float red[4][64];            // per warp and row
-    float mine[4][64];           // a warp's own copy of a value per row
+    float red[8][32];            // a warp's result per row of its group
+    float mine[8][32];           // a warp's own copy of a value per row of its group
 };
 static_assert(sizeof(Small) <= 3072, "small tables");
 
@@ -264,21 +263,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // A 64-row accumulator (16 lanes of each sub-partition): thread l of the warp gets
-// row l % 16 of the sub-partition, columns [0, C) (l < 16) or [C, 2 C).
-__device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
+// row l % 16 of the sub-partition, 16 columns from taddr (l < 16) or the next 16.
 __device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
@@ -291,22 +276,22 @@ __device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Combines v[c] over the 16 lanes of the half warp, per column c, by halving
-// (C - C / 16 shuffles instead of 4 C): lane l ends up with the results of
-// columns NPL l .. + NPL - 1 of all 2 C in v[0], v[1].
-template <bool MAX, int C>
-__device__ __forceinline__ void across_lanes(float (&v)[C], int lane) {
+// Combines v[c] over the 16 lanes of the half warp, per column c, by halving (15
+// shuffles instead of 4 * 16): lane l gets the result of column l of the two
+// halves' 32.
+template <bool MAX>
+__device__ __forceinline__ float across_lanes(float (&v)[16], int lane) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
-        const int n = o * C / 16;
         const bool up = (lane & o) != 0;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
             const float other = __shfl_xor_sync(0xffffffffu, send, o);
             v[i] = MAX ? fmaxf(keep, other) : keep + other;
         }
     }
+    return v[0];
 }
 
 template <int R, int DV, bool PE>
@@ -576,45 +561,38 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_wait(&z.drain[1], 0, 1u << 20);
         }
     } else {
-        // ---------------- softmax and output: key r of the tile, rows C half .. + C - 1 of
-        // the row tile; the statistics of rows NPL lane .. in every warp alike ----------------
-        constexpr int C = L::C, NPL = L::NPL;
-        const int t = 32 * warp + lane, half = lane >> 4, r = 16 * warp + (lane & 15);
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        // ---------------- softmax and output: key r of the tile, rows 16 half .. + 15 of the
+        // warp's group of 32; the statistics of the group's row `lane` in each of its warps ----------------
+        const int cg = warp >> 2, qd = warp & 3;
+        const int t = 32 * qd + lane, half = lane >> 4, r = 16 * qd + (lane & 15);
+        const uint32_t lanes = tmem + ((uint32_t)(32 * qd) << 16) + 32 * cg;
         float *mine = z.mine[warp];
-        const float *mine_c = mine + C * half;
+        const float *mine_c = mine + 16 * half;
+        float (*red)[32] = z.red + 4 * cg;
         int tiles = 0;
         bool ok = true;
         int4 meta[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
         long long at0 = u0;                                              // units of the range before the segment
         for (; w.more() && ok;) {
-            const int rows = min(R, w.s.rows() - w.i * R);               // of this row tile
+            const int rows = min(R, w.s.rows() - w.i * R) - 32 * cg;     // of this group
             const int end = w.s.keys_of(w.i);
-            int sees[NPL], least = 0x7fffffff;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const int row = NPL * lane + i;
-                sees[i] = row < rows ? w.s.sees(w.i * R + row) : 0;
-                if (row < rows) least = min(least, sees[i]);
-            }
-            least = __reduce_min_sync(0xffffffffu, least);
+            const int sees = lane < rows ? w.s.sees(w.i * R + 32 * cg + lane) : 0;
+            const int least = __reduce_min_sync(0xffffffffu, lane < rows ? sees : 0x7fffffff);
             // the sequence's pages, all of them: every block that has a piece of it comes to the same answer
             bool bad = false;
             for (int p = t; (long long)p * a.page_size < w.s.kv; p += 128) {
                 const int pg = a.table[(long long)w.n * a.max_pages + p];
                 bad |= pg < 0 || pg >= a.num_pages;
             }
-            float m_run[NPL], l[C];
+            float m_run = -INFINITY, l[16];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) m_run[i] = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < C; ++c) l[c] = 0.f;
+            for (int c = 0; c < 16; ++c) l[c] = 0.f;
             for (int j = w.j0; j < w.j1; ++j) {
                 // S^T of this tile is there; O^T, P^T and the maxima of the previous one are done with
                 uint64_t *bar = lane == 0 ? &z.s_full[tiles & 1] : lane == 1 && tiles > 0 ? &z.o_full : nullptr;
                 ok = ok && warp_wait(bar, lane == 0 ? (tiles >> 1) & 1 : (tiles - 1) & 1, abort_flag);
                 tc_fence_after();
-                float x[C], y[C];
+                float x[16], y[16];
                 tmem_ld_half(lanes + ((uint32_t)(16 * (tiles & 1)) << 16), x);
                 tmem_wait_ld();
                 tc_fence_before();
@@ -623,73 +601,61 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int key = j * KT + r;
                 if (j * KT + KT > least) {
                     // some row does not see the whole tile
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i) mine[NPL * lane + i] = __int_as_float(sees[i]);
+                    mine[lane] = __int_as_float(sees);
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < C; ++c) x[c] = key < __float_as_int(mine_c[c]) ? x[c] * a.sl2 : -INFINITY;
+                    for (int c = 0; c < 16; ++c) x[c] = key < __float_as_int(mine_c[c]) ? x[c] * a.sl2 : -INFINITY;
                     __syncwarp();
                 } else {
 #pragma unroll
-                    for (int c = 0; c < C; ++c) x[c] *= a.sl2;
+                    for (int c = 0; c < 16; ++c) x[c] *= a.sl2;
                 }
 #pragma unroll
-                for (int c = 0; c < C; ++c) y[c] = x[c];
-                across_lanes<true, C>(y, lane);
-#pragma unroll
-                for (int i = 0; i < NPL; ++i) z.red[warp][NPL * lane + i] = y[i];
-                if (named_bar_or(1, 128, !ok)) { ok = false; break; }
-                bool any = false;
-                float f[NPL];
-#pragma unroll
-                for (int i = 0; i < NPL; ++i) {
-                    const int row = NPL * lane + i;
-                    const float mt = fmaxf(fmaxf(z.red[0][row], z.red[1][row]), fmaxf(z.red[2][row], z.red[3][row]));
-                    // the reference is raised only when the maximum has outgrown it by 2^TH
-                    const bool raise = mt > m_run[i] + TH || (m_run[i] == -INFINITY && mt > -INFINITY);
-                    f[i] = raise ? exp2f(m_run[i] - mt) : 1.f;
-                    if (raise) m_run[i] = mt;
-                    any |= raise;
-                    mine[row] = m_run[i] == -INFINITY ? 0.f : m_run[i];
-                }
-                any = __any_sync(0xffffffffu, any) && j > w.j0;
+                for (int c = 0; c < 16; ++c) y[c] = x[c];
+                red[qd][lane] = across_lanes<true>(y, lane);
+                if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
+                const float mt = fmaxf(fmaxf(red[0][lane], red[1][lane]), fmaxf(red[2][lane], red[3][lane]));
+                // the reference is raised only when the maximum has outgrown it by 2^TH
+                const bool raise = mt > m_run + TH || (m_run == -INFINITY && mt > -INFINITY);
+                const float f = raise ? exp2f(m_run - mt) : 1.f;
+                if (raise) m_run = mt;
+                const bool any = __any_sync(0xffffffffu, raise) && j > w.j0;
+                mine[lane] = m_run == -INFINITY ? 0.f : m_run;
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < C; ++c) x[c] = prep::ex2_approx(x[c] - mine_c[c]);
+                for (int c = 0; c < 16; ++c) x[c] = prep::ex2_approx(x[c] - mine_c[c]);
                 if (any) {
                     __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i) mine[NPL * lane + i] = f[i];
+                    mine[lane] = f;
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < C; ++c) l[c] *= mine_c[c];
-                    for (int m = 0; m < L::MT * NPL; ++m) {
+                    for (int c = 0; c < 16; ++c) l[c] *= mine_c[c];
+                    for (int m = 0; m < L::MT; ++m) {
                         float o[32];
-                        tmem_ld32(lanes + L::O_COL + m * 32, o);
+                        tmem_ld32(lanes + L::O_COL + m * R, o);
                         tmem_wait_ld();
-                        const float *fm = mine + 32 * (m % NPL);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] *= fm[c];
-                        tmem_st32(lanes + L::O_COL + m * 32, o);
+                        for (int c = 0; c < 32; ++c) o[c] *= mine[c];
+                        tmem_st32(lanes + L::O_COL + m * R, o);
                     }
                     tmem_wait_st();
                 }
                 unsigned char *P = sm + L::P_OFF;
 #pragma unroll
-                for (int g = 0; g < C / 8; ++g)
-                    *reinterpret_cast<uint4 *>(P + L::p_off(r, C / 8 * half + g)) =
+                for (int g = 0; g < 2; ++g)
+                    *reinterpret_cast<uint4 *>(P + L::p_off(r, 4 * cg + 2 * half + g)) =
                         make_uint4(pack_bf16(x[8 * g], x[8 * g + 1]), pack_bf16(x[8 * g + 2], x[8 * g + 3]),
                                    pack_bf16(x[8 * g + 4], x[8 * g + 5]), pack_bf16(x[8 * g + 6], x[8 * g + 7]));
 #pragma unroll
-                for (int c = 0; c < C; ++c) l[c] += x[c];
+                for (int c = 0; c < 16; ++c) l[c] += x[c];
                 if (key >= end) {
                     // rows that hold no key of this row tile may hold anything: 0 * NaN is not 0
-                    int s = (int)((long long)tiles * L::MT % L::NS);
-                    for (int m = 0; m < L::MT; ++m) {
+                    const int s0 = (int)((long long)tiles * L::MT % L::NS);
+                    for (int m = cg; m < L::MT; m += L::CG) {
+                        const int s = s0 + m < L::NS ? s0 + m : s0 + m - L::NS;
                         unsigned char *v = sm + L::ST_OFF + s * L::STAGE + half * L::HALF + r * 128;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(v + 16 * e) = make_uint4(0, 0, 0, 0);
-                        if (++s == L::NS) s = 0;
                     }
                 }
                 fence_proxy_async_smem();
@@ -701,55 +667,37 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             ok = wait_on(&z.o_full, (tiles - 1) & 1, abort_flag);
             tc_fence_after();
-            across_lanes<false, C>(l, lane);
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) z.red[warp][NPL * lane + i] = l[i];
-            if (named_bar_or(1, 128, !ok)) { ok = false; break; }
-            float sum[NPL];
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const int row = NPL * lane + i;
-                sum[i] = (z.red[0][row] + z.red[1][row]) + (z.red[2][row] + z.red[3][row]);
-            }
-            bad = named_bar_or(1, 128, bad);
+            red[qd][lane] = across_lanes<false>(l, lane);
+            if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
+            const float sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+            bad = named_bar_or(1 + cg, 128, bad);
             if (bad && tid == 0) set_device_error(a.err, paged::kErrBadPage);
             const long long row0 = (long long)w.s.first * a.H + (long long)w.i * R;
             if (w.j0 == 0 && w.j1 == w.tiles) {
                 // the whole row tile was here
-#pragma unroll
-                for (int i = 0; i < NPL; ++i) {
-                    const int row = NPL * lane + i;
-                    mine[row] = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
-                    if (a.lse && warp == 0 && row < rows && !bad)
-                        a.lse[row0 + row] = sum[i] > 0.f ? (m_run[i] + log2f(sum[i])) * 0.693147180559945f : -INFINITY;
-                }
+                mine[lane] = sum > 0.f ? 1.f / sum : 0.f;
+                if (a.lse && qd == 0 && lane < rows && !bad)
+                    a.lse[row0 + 32 * cg + lane] = sum > 0.f ? (m_run + log2f(sum)) * 0.693147180559945f : -INFINITY;
                 __syncwarp();
                 if (!bad)
-                    for (int m = 0; m < L::MT * NPL; ++m) {
+                    for (int m = 0; m < L::MT; ++m) {
                         float o[32];
-                        tmem_ld32(lanes + L::O_COL + m * 32, o);
+                        tmem_ld32(lanes + L::O_COL + m * R, o);
                         tmem_wait_ld();
-                        const int c0 = 32 * (m % NPL), ch = 128 * (m / NPL) + t;
+                        __nv_bfloat16 *dst = a.out + (row0 + 32 * cg) * DV + 128 * m + t;
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (c0 + c < rows)
-                                a.out[(row0 + c0 + c) * DV + ch] = __float2bfloat16_rn(o[c] * mine[c0 + c]);
+                            if (c < rows) dst[(size_t)c * DV] = __float2bfloat16_rn(o[c] * mine[c]);
                     }
             } else {
                 // a piece: slot 0 if it continues the row tile, slot 1 if it begins it
-                const int slot = 2 * b + (w.j0 == 0 ? 1 : 0);
-                if (warp == 0)
-#pragma unroll
-                    for (int i = 0; i < NPL; ++i) {
-                        float *ml = a.ws_ml + ((size_t)slot * R + NPL * lane + i) * 2;
-                        ml[0] = m_run[i];
-                        ml[1] = bad ? -1.f : sum[i];
-                    }
-                for (int m = 0; m < L::MT * NPL; ++m) {
+                const size_t at = (size_t)(2 * b + (w.j0 == 0 ? 1 : 0)) * R + 32 * cg;
+                if (qd == 0) *reinterpret_cast<float2 *>(a.ws_ml + (at + lane) * 2) = make_float2(m_run, bad ? -1.f : sum);
+                for (int m = 0; m < L::MT; ++m) {
                     float o[32];
-                    tmem_ld32(lanes + L::O_COL + m * 32, o);
+                    tmem_ld32(lanes + L::O_COL + m * R, o);
                     tmem_wait_ld();
-                    float *dst = a.ws_o + ((size_t)slot * R + 32 * (m % NPL)) * DV + 128 * (m / NPL) + t;
+                    float *dst = a.ws_o + at * DV + 128 * m + t;
 #pragma unroll
                     for (int c = 0; c < 32; ++c) dst[(size_t)c * DV] = o[c];
                 }
@@ -758,7 +706,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const long long first = at0 - w.at + OV, last = first + w.tiles - 1;
                     auto block_of = [&](long long u) { return (int)((u * G + G - 1) / total); };
                     const int b0 = w.j0 == 0 ? b : block_of(first);
-                    meta[w.j0 == 0 ? 1 : 0] = make_int4((int)row0, rows, b0, block_of(last) - b0 + 1);
+                    meta[w.j0 == 0 ? 1 : 0] = make_int4((int)row0, min(R, w.s.rows() - w.i * R), b0, block_of(last) - b0 + 1);
                 }
             }
             tc_fence_before();
