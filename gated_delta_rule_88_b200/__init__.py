@@ -558,30 +558,62 @@ def kda_state_affine(M, B, S_in, out=None):
 
 
 _ATTN_FULL, _ROPE_INTERLEAVED, _ROPE_INVERSE = 8, 16, 32
+_DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+
+# The calls below run once a layer in every decoding step, where a few
+# microseconds on the host count: plain integers for pointers, one check a
+# tensor, and the device is switched only when it is another one.
 
 
-def _paged_args(who, T, cache, page_table, kv_lens, cu_seqlens, dev, dt, dk):
-    """Checks the cache's arrays; (num_seqs, num_pages, page_size, max_pages, page_stride)."""
+def _on(t, name, idx, dtype):
+    """A contiguous tensor of the type on CUDA device idx."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != idx or not t.is_contiguous():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.get_device() != idx:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{idx}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn, idx, *args):
+    """fn(*args, stream) with CUDA device idx current, on its current stream."""
+    if torch._C._cuda_getDevice() == idx:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
+    if rc:
+        _check(rc)
+
+
+def _paged_args(who, T, cache, page_table, kv_lens, cu_seqlens, idx, dt, dk):
+    """Checks the cache's arrays; pointers (cache, page_table, kv_lens, cu_seqlens)
+    and sizes (num_seqs, num_pages, page_size, max_pages, page_stride)."""
     if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != dk:
         raise ValueError(f"{who}: cache must be [num_pages, page_size, {dk}]")
-    if cache.device != dev or cache.dtype != dt:
-        raise TypeError(f"{who}: cache must be {dt} on {dev}")
-    if cache.stride(2) != 1 or cache.stride(1) != dk:
+    if cache.get_device() != idx or cache.dtype is not dt:
+        raise TypeError(f"{who}: cache must be {dt} on cuda:{idx}")
+    pages, psize, _ = cache.shape
+    stride, row, one = cache.stride()
+    if one != 1 or row != dk:
         raise ValueError(f"{who}: the rows of a page must be contiguous")
-    _need(page_table, "page_table", dev, torch.int32)
-    _need(kv_lens, "kv_lens", dev, torch.int32)
+    if pages <= 1:
+        stride = psize * dk                    # (a pool of one page may report any stride)
+    tp, lp = _on(page_table, "page_table", idx, torch.int32), _on(kv_lens, "kv_lens", idx, torch.int32)
     N = kv_lens.numel()
     if page_table.dim() != 2 or page_table.shape[0] != N or kv_lens.dim() != 1:
         raise ValueError(f"{who}: page_table must be [num_seqs, max_pages] and kv_lens [num_seqs]")
+    cp = None
     if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", dev, torch.int32)
-        if tuple(cu_seqlens.shape) != (N + 1,):
+        cp = _on(cu_seqlens, "cu_seqlens", idx, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() != N + 1:
             raise ValueError(f"{who}: cu_seqlens must be [{N + 1}]")
     elif N == 0 or T % N:
         raise ValueError(f"{who}: without cu_seqlens the tokens must divide evenly over the sequences")
-    # (a pool of one page may report any stride)
-    stride = cache.stride(0) if cache.shape[0] > 1 else cache.shape[1] * dk
-    return N, cache.shape[0], cache.shape[1], page_table.shape[1], stride
+    return (cache.data_ptr(), tp, lp, cp), (N, pages, psize, page_table.shape[1], stride)
 
 
 def kda_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=None, out=None, lse=None,
@@ -592,37 +624,31 @@ def kda_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=Non
     [N,max_pages], kv_lens [N] (new tokens included), cu_seqlens [N+1] or None
     (T / N tokens each), all int32.  scale: default dk ** -0.5.  causal: a token
     sees the keys up to its own position, else all of its sequence's.
-    Returns (out [T,H,dv], lse [T,H] fp32); allocated here, rows behind the
-    last sequence are unspecified."""
-    lib = load_library()
-    dev = q.device
-    if dev.type != "cuda":
+    Returns (out [T,H,dv], lse [T,H] fp32); where they are allocated here, rows
+    behind the last sequence are unspecified."""
+    lib = _lib or load_library()
+    idx = q.get_device()
+    if idx < 0:
         raise ValueError("kda_latent_attn needs CUDA tensors (no CPU path)")
     if q.dim() != 3:
         raise ValueError("q must be [T,H,dk]")
     T, H, dk = q.shape
-    _need(q, "q", dev)
-    N, pages, psize, mp, ps = _paged_args("kda_latent_attn", T, cache, page_table, kv_lens, cu_seqlens, dev, q.dtype, dk)
+    dt = q.dtype
+    qp = _on(q, "q", idx, dt)
+    (cp, tp, lp, up), sizes = _paged_args("kda_latent_attn", T, cache, page_table, kv_lens, cu_seqlens, idx, dt, dk)
     if out is None:
-        out = torch.empty(T, H, dv, dtype=q.dtype, device=dev)
-    else:
-        _need(out, "out", dev, q.dtype)
-        if tuple(out.shape) != (T, H, dv):
-            raise ValueError(f"out must be [{T},{H},{dv}]")
+        out = q.new_empty((T, H, dv))
+    elif out.shape != (T, H, dv):
+        raise ValueError(f"out must be [{T},{H},{dv}]")
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", dev, torch.float32)
-        if tuple(lse.shape) != (T, H):
-            raise ValueError(f"lse must be [{T},{H}]")
+        lse = q.new_empty((T, H), dtype=torch.float32)
+    elif lse.shape != (T, H):
+        raise ValueError(f"lse must be [{T},{H}]")
+    op, sp = _on(out, "out", idx, dt), _on(lse, "lse", idx, torch.float32)
     if T == 0:
         return out, lse
-    with torch.cuda.device(dev):
-        rc = lib.kda_latent_attn(_dptr(q), _dptr(cache), _dptr(page_table), _dptr(kv_lens), _dptr(cu_seqlens),
-                                 _dptr(out), _dptr(lse), T, H, dk, int(dv), N, pages, psize, mp, ps,
-                                 float(dk ** -0.5 if scale is None else scale), 0 if causal else _ATTN_FULL,
-                                 _dtype_code(q), _stream_handle(dev))
-    _check(rc)
+    _call(lib.kda_latent_attn, idx, qp, cp, tp, lp, up, op, sp, T, H, dk, dv, *sizes,
+          dk ** -0.5 if scale is None else scale, 0 if causal else _ATTN_FULL, _DTYPES.get(dt, -1))
     return out, lse
 
 
@@ -633,46 +659,46 @@ def kda_latent_append(kv, cache, page_table, kv_lens, q_pe=None, q=None, freqs=N
     turned by the token's position, and q_pe [T,H,rot] (tokens and heads may be
     strided) likewise into q[..., dk-rot:] of q [T,H,dk].  Other arguments as
     kda_latent_attn."""
-    lib = load_library()
-    dev = kv.device
-    if dev.type != "cuda":
+    lib = _lib or load_library()
+    idx = kv.get_device()
+    if idx < 0:
         raise ValueError("kda_latent_append needs CUDA tensors (no CPU path)")
-    if kv.dim() != 2 or (kv.shape[0] > 0 and kv.stride(1) != 1):
-        raise ValueError("kv must be [T,dk] with contiguous rows")
+    if kv.dim() != 2:
+        raise ValueError("kv must be [T,dk]")
     T, dk = kv.shape
-    N, pages, psize, mp, ps = _paged_args("kda_latent_append", T, cache, page_table, kv_lens, cu_seqlens, dev, kv.dtype, dk)
+    dt = kv.dtype
+    kvs, one = kv.stride()
+    if T and (one != 1 or (T > 1 and kvs < dk)):
+        raise ValueError("kv must have contiguous rows, one after the other")
+    (cp, tp, lp, up), sizes = _paged_args("kda_latent_append", T, cache, page_table, kv_lens, cu_seqlens, idx, dt, dk)
     H, rot, ts, hs = 1, 0, 0, 0
+    fp = pp = qp = None
     if freqs is not None:
-        _need(freqs, "freqs", dev, torch.float32)
+        fp = _on(freqs, "freqs", idx, torch.float32)
         rot = 2 * freqs.numel()
     if (q_pe is None) != (q is None):
         raise ValueError("q_pe and q come together")
     if q_pe is not None:
-        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.device != dev or q_pe.dtype != kv.dtype:
-            raise ValueError(f"q_pe must be [{T},H,rot] {kv.dtype} on {dev}")
-        H = q_pe.shape[1]
-        if freqs is not None and q_pe.shape[2] != rot:
+        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.get_device() != idx or q_pe.dtype is not dt:
+            raise ValueError(f"q_pe must be [{T},H,rot] {dt} on cuda:{idx}")
+        _, H, width = q_pe.shape
+        if freqs is not None and width != rot:
             raise ValueError(f"q_pe must have {rot} channels, twice as many as freqs")
-        rot = q_pe.shape[2]
-        if q_pe.numel() and q_pe.stride(2) != 1:
+        rot = width
+        ts, hs, one = q_pe.stride()
+        if T and H and one != 1:
             raise ValueError("the heads of q_pe must be contiguous")
-        ts, hs = q_pe.stride(0) if T > 1 else 0, q_pe.stride(1) if H > 1 else 0
-        if ts == 0 and T > 1 or hs == 0 and H > 1:
+        if (ts == 0 and T > 1) or (hs == 0 and H > 1):
             raise ValueError("q_pe must not be broadcast")
-        _need(q, "q", dev, kv.dtype)
-        if tuple(q.shape) != (T, H, dk):
+        ts, hs = ts if T > 1 else 0, hs if H > 1 else 0
+        pp, qp = q_pe.data_ptr(), _on(q, "q", idx, dt)
+        if q.shape != (T, H, dk):
             raise ValueError(f"q must be [{T},{H},{dk}]")
-    kvs = kv.stride(0) if T > 1 else 0
-    if T > 1 and kvs == 0:
-        raise ValueError("kv must not be broadcast")
     if T == 0:
         return
-    with torch.cuda.device(dev):
-        rc = lib.kda_latent_append(_dptr(kv), _dptr(cache), _dptr(page_table), _dptr(kv_lens), _dptr(cu_seqlens),
-                                   _dptr(q_pe), _dptr(q), _dptr(freqs), T, H, dk, rot, N, pages, psize, mp, ps, kvs,
-                                   ts, hs, _ROPE_INTERLEAVED if interleaved else 0, float(scale), _dtype_code(kv),
-                                   _stream_handle(dev))
-    _check(rc)
+    N, pages, psize, mp, stride = sizes
+    _call(lib.kda_latent_append, idx, kv.data_ptr(), cp, tp, lp, up, pp, qp, fp, T, H, dk, rot, N, pages, psize, mp, stride,
+          kvs if T > 1 else 0, ts, hs, _ROPE_INTERLEAVED if interleaved else 0, scale, _DTYPES.get(dt, -1))
 
 
 def kda_rope(x, positions, freqs, out=None, offset: int = 0, interleaved: bool = False, inverse: bool = False,
@@ -682,49 +708,50 @@ def kda_rope(x, positions, freqs, out=None, offset: int = 0, interleaved: bool =
     positions int32 [T]; freqs fp32: radians a position of each pair (i, i +
     len(freqs)), or (2i, 2i + 1) if interleaved.  inverse: the transposed map,
     i.e. the gradient.  out may be x (in place)."""
-    lib = load_library()
-    dev = x.device
-    if dev.type != "cuda":
+    lib = _lib or load_library()
+    idx = x.get_device()
+    if idx < 0:
         raise ValueError("kda_rope needs CUDA tensors (no CPU path)")
     if x.dim() != 3:
         raise ValueError("x must be [T,H,d]")
     T, H, d = x.shape
 
     def stride(t, name):
-        if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+        ts, hs, one = t.stride()
+        if t.numel() and (one != 1 or (H > 1 and hs != d)):
             raise ValueError(f"the heads of {name} must be contiguous")
-        if T > 1 and t.stride(0) == 0:
+        if T <= 1:
+            return H * d
+        if ts == 0:
             raise ValueError(f"{name} must not be broadcast")
-        return t.stride(0) if T > 1 else H * d
+        return ts
 
     xs = stride(x, "x")
-    _need(positions, "positions", dev, torch.int32)
-    _need(freqs, "freqs", dev, torch.float32)
-    if tuple(positions.shape) != (T,) or freqs.dim() != 1:
+    pp, fp = _on(positions, "positions", idx, torch.int32), _on(freqs, "freqs", idx, torch.float32)
+    if positions.shape != (T,) or freqs.dim() != 1:
         raise ValueError(f"positions must be [{T}] and freqs [rot / 2]")
     if out is None:
-        out = torch.empty(T, H, d, dtype=x.dtype, device=dev)
-    elif tuple(out.shape) != (T, H, d) or out.device != dev or out.dtype != x.dtype:
-        raise ValueError(f"out must be [{T},{H},{d}] {x.dtype} on {dev}")
-    code = _dtype_code(x)
+        out = x.new_empty((T, H, d))
+    elif out.shape != (T, H, d) or out.get_device() != idx or out.dtype is not x.dtype:
+        raise ValueError(f"out must be [{T},{H},{d}] {x.dtype} on cuda:{idx}")
     if T == 0:
         return out
-    with torch.cuda.device(dev):
-        rc = lib.kda_rope(_dptr(x), _dptr(positions), _dptr(freqs), _dptr(out), T, H, d, 2 * freqs.numel(), int(offset),
-                          xs, stride(out, "out"), (_ROPE_INTERLEAVED if interleaved else 0) |
-                          (_ROPE_INVERSE if inverse else 0), float(scale), code, _stream_handle(dev))
-    _check(rc)
+    _call(lib.kda_rope, idx, x.data_ptr(), pp, fp, out.data_ptr(), T, H, d, 2 * freqs.numel(), offset, xs,
+          stride(out, "out"), (_ROPE_INTERLEAVED if interleaved else 0) | (_ROPE_INVERSE if inverse else 0), scale,
+          _DTYPES.get(x.dtype, -1))
     return out
 
 
 def _pool_args(who, pool, planes):
-    """(planes, num_pages, page_bytes) of a contiguous pool [pages, ...] or [planes, pages, ...]."""
-    if not isinstance(pool, torch.Tensor) or pool.device.type != "cuda":
+    """(device index, planes, num_pages, page_bytes) of a contiguous pool [pages, ...] or [planes, pages, ...]."""
+    idx = pool.get_device() if isinstance(pool, torch.Tensor) else -1
+    if idx < 0:
         raise ValueError(f"{who} needs CUDA tensors (no CPU path)")
-    if pool.dim() < (3 if planes else 2) or not pool.is_contiguous() or pool.numel() == 0:
+    numel = pool.numel()
+    if pool.dim() < (3 if planes else 2) or numel == 0 or not pool.is_contiguous():
         raise ValueError(f"{who}: the pool must be a contiguous, non-empty [{'planes, ' if planes else ''}pages, ...]")
     n, p = (pool.shape[0], pool.shape[1]) if planes else (1, pool.shape[0])
-    return n, p, pool.numel() // (n * p) * pool.element_size()
+    return idx, n, p, numel // (n * p) * pool.element_size()
 
 
 def kda_pages_copy(pool, src, dst, planes: bool = False) -> None:
@@ -733,16 +760,12 @@ def kda_pages_copy(pool, src, dst, planes: bool = False) -> None:
     zeros for src[i] = -1.  src, dst int32 [n], n <= 4096; sources and
     destinations may overlap in any way; the last move to a destination counts.
     Works on a latent cache and on the state pool of kda_recurrent_steps."""
-    lib = load_library()
-    n, p, nbytes = _pool_args("kda_pages_copy", pool, planes)
-    dev = pool.device
-    _need(src, "src", dev, torch.int32)
-    _need(dst, "dst", dev, torch.int32)
+    lib = _lib or load_library()
+    idx, n, p, nbytes = _pool_args("kda_pages_copy", pool, planes)
+    sp, dp = _on(src, "src", idx, torch.int32), _on(dst, "dst", idx, torch.int32)
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be [n]")
-    with torch.cuda.device(dev):
-        rc = lib.kda_pages_copy(_dptr(pool), _dptr(src), _dptr(dst), src.numel(), n, p, nbytes, _stream_handle(dev))
-    _check(rc)
+    _call(lib.kda_pages_copy, idx, pool.data_ptr(), sp, dp, src.numel(), n, p, nbytes)
 
 
 def kda_pages_compact(pool, pages, planes: bool = False, out=None):
@@ -751,20 +774,14 @@ def kda_pages_compact(pool, pages, planes: bool = False, out=None):
     table; negative entries are padding; a page may be listed several times).
     With n distinct live pages, those at n and beyond go to the free indexes
     below n, both in ascending order.  out may be ``pages``."""
-    lib = load_library()
-    n, p, nbytes = _pool_args("kda_pages_compact", pool, planes)
-    dev = pool.device
-    _need(pages, "pages", dev, torch.int32)
+    lib = _lib or load_library()
+    idx, n, p, nbytes = _pool_args("kda_pages_compact", pool, planes)
+    pp = _on(pages, "pages", idx, torch.int32)
     if out is None:
         out = torch.empty_like(pages)
-    else:
-        _need(out, "out", dev, torch.int32)
-        if out.shape != pages.shape:
-            raise ValueError("out must have the shape of pages")
-    with torch.cuda.device(dev):
-        rc = lib.kda_pages_compact(_dptr(pool), _dptr(pages), _dptr(out), pages.numel(), n, p, nbytes,
-                                   _stream_handle(dev))
-    _check(rc)
+    elif out.shape != pages.shape:
+        raise ValueError("out must have the shape of pages")
+    _call(lib.kda_pages_compact, idx, pool.data_ptr(), pp, _on(out, "out", idx, torch.int32), pages.numel(), n, p, nbytes)
     return out
 
 
