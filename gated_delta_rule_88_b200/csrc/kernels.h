@@ -159,7 +159,7 @@ cudaError_t launch_rope(const void *x, const int32_t *positions, const float *fr
 
 // Page moves within a pool [planes, num_pages, page_bytes] (pages.cu).
 cudaError_t launch_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int count, int planes,
-                              int num_pages, long long page_bytes, int *err, cudaStream_t st);
+                              int num_pages, long long page_bytes, int sms, int *err, cudaStream_t st);
 size_t pages_compact_scratch_bytes(int num_pages);
 cudaError_t launch_pages_compact(void *pool, const int32_t *pages, int32_t *new_pages, long long count,
                                  int planes, int num_pages, long long page_bytes, int *scratch, int sms, int *err,

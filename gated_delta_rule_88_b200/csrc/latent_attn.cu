@@ -308,6 +308,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         return;
     }
 
+    paged::let_next_start();
     // ---- this block's range of the (row tile, key tile) units
     const int per = (a.N + L::NT - 1) / L::NT;
     const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
@@ -735,13 +736,14 @@ constexpr int FEW = 8;                         // pieces that one warp takes
 
 template <int R, int DV>
 __global__ void __launch_bounds__(32 * CW)
-latent_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_ml, const int4 *__restrict__ meta,
-                      __nv_bfloat16 *__restrict__ out, float *__restrict__ lse)
+latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta,
+                      __nv_bfloat16 *out, float *lse)
 {
     constexpr int V = DV / 128;                // float4's of a lane
     __shared__ float4 part[CW][DV / 4];
     __shared__ float part_l[CW];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    paged::wait_for_previous();
     for (int e = 0; e < 2; ++e) {
         const int4 mt = meta[2 * blockIdx.x + e];
         if (mt.w == 0) continue;
@@ -850,8 +852,8 @@ cudaError_t launch_t(const void *q, const void *cache, const PagedPlan &p, void 
     if (e != cudaSuccess) return e;
     latent_attn_kernel<R, DV, PE><<<sms, L::NT, smem, st>>>(mq, mc, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    latent_combine_kernel<R, DV><<<dim3(sms, 4), 32 * CW, 0, st>>>(a.ws_o, a.ws_ml, a.meta, a.out, lse);
-    return cudaGetLastError();
+    return paged::launch_after(latent_combine_kernel<R, DV>, dim3(sms, 4), dim3(32 * CW), 0, st, a.ws_o, a.ws_ml, a.meta,
+                               a.out, lse);
 }
 
 // rows of a tile: 32 when a sequence has no more than that on average (one token of 32 heads), else 64

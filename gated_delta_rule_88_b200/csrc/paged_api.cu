@@ -96,6 +96,7 @@ kda_status kda_latent_append(const void *kv, void *cache, const int32_t *page_ta
     if (q_pe_ts == 0) q_pe_ts = (long long)H * q_pe_hs;
     if (kv_stride == 0) kv_stride = dk;
     const long long lim = 1LL << 38;
+    if ((long long)H * dk > (1 << 24)) return fail(KDA_ERR_INVALID_ARG, "%s: H * dk = %lld exceeds 2^24", fn, (long long)H * dk);
     if (dk % 8 || kv_stride % 8 || kv_stride < dk || kv_stride > lim ||
         (q_pe && (q_pe_hs % 8 || q_pe_ts % 8 || q_pe_hs < rot || q_pe_ts < rot || q_pe_hs > lim || q_pe_ts > lim)))
         return fail(KDA_ERR_INVALID_ARG, "%s: dk and the strides must be multiples of 8 that hold a row (dk=%d kv_stride=%lld "
@@ -117,7 +118,7 @@ kda_status kda_rope(const void *x, const int32_t *positions, const float *freqs,
     kda::t_msg[0] = 0;
     const char *fn = "kda_rope";
     if (!x || !positions || !freqs || !out) return fail(KDA_ERR_INVALID_ARG, "%s: null pointer argument", fn);
-    if (T < 0 || H <= 0 || d <= 0 || T > 0x7fffffffLL || (long long)H * d > (1LL << 30))
+    if (T < 0 || H <= 0 || d <= 0 || T > 0x7fffffffLL || d > 65536 || (long long)H * d > (1LL << 30))
         return fail(KDA_ERR_INVALID_ARG, "%s: bad sizes T=%lld H=%d d=%d", fn, T, H, d);
     if (dtype != KDA_F32 && dtype != KDA_BF16) return fail(KDA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
     if (flags & ~(unsigned)(KDA_ROPE_INTERLEAVED | KDA_ROPE_INVERSE))
@@ -165,8 +166,12 @@ kda_status kda_pages_copy(void *pool, const int32_t *src, const int32_t *dst, in
     if (count == 0) return KDA_OK;
     if (!src || !dst) return fail(KDA_ERR_INVALID_ARG, "%s: null pointer argument", fn);
     if (!aligned4(src) || !aligned4(dst)) return fail(KDA_ERR_INVALID_ARG, "%s: src and dst must be 4-byte aligned", fn);
-    cudaError_t e = kda::launch_pages_copy(pool, src, dst, count, planes, num_pages, page_bytes, kda::error_word(),
-                                           (cudaStream_t)stream);
+    cudaMemPool_t mp;
+    int sms = 148;
+    cudaError_t e = kda::get_pool(&mp, &sms);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_pages_copy device");
+    e = kda::launch_pages_copy(pool, src, dst, count, planes, num_pages, page_bytes, sms, kda::error_word(),
+                               (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "kda_pages_copy launch");
     return KDA_OK;
 }

@@ -17,40 +17,44 @@ namespace {
 
 constexpr int NT = 256;
 
-// Shared memory of a CTA of the copy: the moves' data, then a hash table
-// {destination, last move to it} of `slots` entries (a power of two >= 2 count).
+// Shared memory of a CTA: the moves' data, (source, destination) of each move
+// that counts, and a hash table {destination, last move to it} of `slots` entries
+// (a power of two >= 2 count).  piece = 16 << lsh bytes.
 __global__ void __launch_bounds__(NT)
 pages_copy_kernel(unsigned char *pool, const int32_t *__restrict__ src, const int32_t *__restrict__ dst,
-                  int count, int num_pages, long long page_bytes, int piece, int slots, int *err)
+                  int count, int num_pages, long long page_bytes, int lsh, int slots, int *err)
 {
     extern __shared__ __align__(16) unsigned char sm[];
-    int *key = reinterpret_cast<int *>(sm + (size_t)count * piece);
+    int2 *move = reinterpret_cast<int2 *>(sm + ((size_t)count << (lsh + 4)));
+    int *key = reinterpret_cast<int *>(move + count);
     int *last = key + slots;
-    const long long at = (long long)blockIdx.x * piece;
-    const int lanes = (int)min((long long)piece, page_bytes - at) / 16;      // 16-byte lanes of the range
+    const long long at = (long long)blockIdx.x << (lsh + 4);
+    const int lanes = (int)min(1LL << lsh, (page_bytes - at) / 16);          // 16-byte lanes of the range
     unsigned char *base = pool + (long long)blockIdx.y * num_pages * page_bytes + at;
-    for (int i = threadIdx.x; i < slots; i += NT) { key[i] = -1; last[i] = -1; }
     bool bad = false;
-    for (int e = threadIdx.x; e < count * lanes; e += NT) {
-        const int i = e / lanes, l = e - i * lanes;
+    for (int i = threadIdx.x; i < count; i += NT) {
         const int s = src[i], d = dst[i];
-        if (d < 0 || d >= num_pages || s < -1 || s >= num_pages) { bad = true; continue; }
-        unsigned char *to = sm + (size_t)i * piece + 16 * l;
-        if (s >= 0) cp_async16(to, base + (long long)s * page_bytes + 16 * l);
+        const bool ok = d >= 0 && d < num_pages && s >= -1 && s < num_pages;
+        bad |= !ok;
+        move[i] = make_int2(s, ok ? d : -1);
+    }
+    for (int i = threadIdx.x; i < slots; i += NT) { key[i] = -1; last[i] = -1; }
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0) set_device_error(err, kErrBadSlot);
+    __syncthreads();
+    for (int e = threadIdx.x; e < count << lsh; e += NT) {
+        const int i = e >> lsh, l = e & ((1 << lsh) - 1);
+        const int2 m = move[i];
+        if (m.y < 0 || l >= lanes) continue;
+        unsigned char *to = sm + (size_t)e * 16;
+        if (m.x >= 0) cp_async16(to, base + (long long)m.x * page_bytes + 16 * l);
         else *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
     }
     cp_async_commit();
-    if (bad && blockIdx.x == 0 && blockIdx.y == 0) set_device_error(err, kErrBadSlot);
-    __syncthreads();
-    // the last valid move to each destination
-    auto valid = [&](int i) {
-        const int s = src[i], d = dst[i];
-        return d >= 0 && d < num_pages && s >= -1 && s < num_pages;
-    };
+    // while the copies land: the last move to each destination is the one that counts
     auto slot_of = [&](int d) { return (int)(((unsigned)d * 2654435761u) & (unsigned)(slots - 1)); };
     for (int i = threadIdx.x; i < count; i += NT) {
-        if (!valid(i)) continue;
-        const int d = dst[i];
+        const int d = move[i].y;
+        if (d < 0) continue;
         int s = slot_of(d);
         // at most count < slots keys: an own or empty entry is found within `slots` probes
         for (int tries = 0; tries < slots; ++tries) {
@@ -60,17 +64,22 @@ pages_copy_kernel(unsigned char *pool, const int32_t *__restrict__ src, const in
         }
         atomicMax(&last[s], i);
     }
-    cp_async_wait<0>();
     __syncthreads();
-    for (int e = threadIdx.x; e < count * lanes; e += NT) {
-        const int i = e / lanes, l = e - i * lanes;
-        if (!valid(i)) continue;
-        const int d = dst[i];
+    for (int i = threadIdx.x; i < count; i += NT) {
+        const int d = move[i].y;
+        if (d < 0) continue;
         int s = slot_of(d);
         for (int tries = 0; tries < slots && key[s] != d; ++tries) s = (s + 1) & (slots - 1);
-        if (last[s] != i) continue;
+        if (last[s] != i) move[i].y = -1;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    for (int e = threadIdx.x; e < count << lsh; e += NT) {
+        const int i = e >> lsh, l = e & ((1 << lsh) - 1);
+        const int d = move[i].y;
+        if (d < 0 || l >= lanes) continue;
         *reinterpret_cast<uint4 *>(base + (long long)d * page_bytes + 16 * l) =
-            *reinterpret_cast<const uint4 *>(sm + (size_t)i * piece + 16 * l);
+            *reinterpret_cast<const uint4 *>(sm + (size_t)e * 16);
     }
 }
 
@@ -85,9 +94,10 @@ compact_plan_kernel(const int32_t *pages, int32_t *new_pages, long long count, i
                     int *err)
 {
     extern __shared__ uint32_t bits[];
+    paged::let_next_start();
     const int words = (num_pages + 31) / 32;
     int *before = reinterpret_cast<int *>(bits + words);          // live pages before each word
-    __shared__ int part[PLAN_NT];
+    __shared__ int part[PLAN_NT / 32];
     const int tid = threadIdx.x;
     int *to = scratch + 64, *from = to + num_pages / 2 + 1;
     for (int w = tid; w < words; w += PLAN_NT) bits[w] = 0;
@@ -104,16 +114,20 @@ compact_plan_kernel(const int32_t *pages, int32_t *new_pages, long long count, i
     const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
     int sum = 0;
     for (int w = w0; w < w1; ++w) sum += __popc(bits[w]);
-    part[tid] = sum;
-    __syncthreads();
-    for (int off = 1; off < PLAN_NT; off <<= 1) {
-        const int x = tid >= off ? part[tid - off] : 0;
-        __syncthreads();
-        part[tid] += x;
-        __syncthreads();
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if ((tid & 31) >= o) incl += x;
     }
-    const int n = part[PLAN_NT - 1];
-    int run = part[tid] - sum;
+    if ((tid & 31) == 31) part[tid >> 5] = incl;
+    __syncthreads();
+    int run = incl - sum, n = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_NT / 32; ++w) {
+        if (w < tid >> 5) run += part[w];
+        n += part[w];
+    }
     for (int w = w0; w < w1; ++w) { before[w] = run; run += __popc(bits[w]); }
     __syncthreads();
     auto live_before = [&](int p) {
@@ -121,15 +135,10 @@ compact_plan_kernel(const int32_t *pages, int32_t *new_pages, long long count, i
     };
     // n <= num_pages; n == num_pages: nothing moves
     const int stay = n < num_pages ? live_before(n) : n;
-    for (int w = w0; w < w1; ++w) {
-        uint32_t x = bits[w];
-        for (int b = 0; b < 32; ++b) {
-            const int p = 32 * w + b;
-            if (p >= num_pages) break;
-            const bool live = (x >> b) & 1u;
-            if (p < n && !live) to[p - live_before(p)] = p;
-            else if (p >= n && live) from[live_before(p) - stay] = p;
-        }
+    for (int p = tid; p < num_pages; p += PLAN_NT) {
+        const bool live = (bits[p >> 5] >> (p & 31)) & 1u;
+        if (p < n && !live) to[p - live_before(p)] = p;
+        else if (p >= n && live) from[live_before(p) - stay] = p;
     }
     if (tid == 0) scratch[0] = n - stay;
     __syncthreads();
@@ -144,9 +153,10 @@ compact_plan_kernel(const int32_t *pages, int32_t *new_pages, long long count, i
 constexpr int PART = NT * 64;
 
 __global__ void __launch_bounds__(NT)
-compact_move_kernel(unsigned char *pool, const int *__restrict__ scratch, int planes, int num_pages,
+compact_move_kernel(unsigned char *pool, const int *scratch, int planes, int num_pages,
                     long long page_bytes, int parts)
 {
+    paged::wait_for_previous();
     const int moves = scratch[0];
     const int *to = scratch + 64, *from = to + num_pages / 2 + 1;
     const long long tasks = (long long)planes * moves * parts;
@@ -172,22 +182,24 @@ compact_move_kernel(unsigned char *pool, const int *__restrict__ scratch, int pl
 size_t pages_compact_scratch_bytes(int num_pages) { return 256 + sizeof(int) * 2 * ((size_t)num_pages / 2 + 1); }
 
 cudaError_t launch_pages_copy(void *pool, const int32_t *src, const int32_t *dst, int count, int planes,
-                              int num_pages, long long page_bytes, int *err, cudaStream_t st)
+                              int num_pages, long long page_bytes, int sms, int *err, cudaStream_t st)
 {
     int slots = 32;
     while (slots < 2 * count) slots <<= 1;
-    // the range of a CTA: up to 64 KB for all moves together, at least 32 bytes
-    // of a page (a DRAM sector)
-    long long piece = (64 * 1024 / count) & ~15;
-    if (piece < 32) piece = 32;
-    if (piece > page_bytes) piece = page_bytes;
-    const long long ranges = (page_bytes + piece - 1) / piece;
+    // The range of a CTA: a power of two, 64 KB for all moves together (three
+    // CTAs an SM), but at least 32 bytes of a page (a DRAM sector); small moves
+    // are spread over the SMs in ranges of down to 256 bytes.
+    int lsh = 1;
+    while (lsh < 12 && ((long long)count << (lsh + 5)) <= 64 * 1024) ++lsh;
+    while (lsh > 4 && ((page_bytes * planes) >> (lsh + 4)) < 4 * sms) --lsh;
+    while (lsh > 0 && (16LL << (lsh - 1)) >= page_bytes) --lsh;
+    const long long ranges = (page_bytes + (16 << lsh) - 1) >> (lsh + 4);
     if (ranges > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)count * piece + 8 * (size_t)slots;
+    const size_t smem = ((size_t)count << (lsh + 4)) + 8 * (size_t)count + 8 * (size_t)slots;
     cudaError_t e = cudaFuncSetAttribute(pages_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     pages_copy_kernel<<<dim3((unsigned)ranges, planes), NT, smem, st>>>((unsigned char *)pool, src, dst, count,
-                                                                        num_pages, page_bytes, (int)piece, slots, err);
+                                                                        num_pages, page_bytes, lsh, slots, err);
     return cudaGetLastError();
 }
 
@@ -202,9 +214,8 @@ cudaError_t launch_pages_compact(void *pool, const int32_t *pages, int32_t *new_
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long parts = (page_bytes + PART - 1) / PART;
     if (parts > 0x7fffffffLL) return cudaErrorInvalidValue;
-    compact_move_kernel<<<8 * sms, NT, 0, st>>>((unsigned char *)pool, scratch, planes, num_pages, page_bytes,
-                                                (int)parts);
-    return cudaGetLastError();
+    return paged::launch_after(compact_move_kernel, dim3(8 * sms), dim3(NT), 0, st, (unsigned char *)pool, scratch, planes,
+                               num_pages, page_bytes, (int)parts);
 }
 
 }  // namespace kda

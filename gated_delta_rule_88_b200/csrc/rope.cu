@@ -28,18 +28,17 @@ __device__ __forceinline__ float2 turn(double position, float freq, float scale,
 template <typename T> struct Piece;
 template <> struct Piece<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, float (&v)[4]) {
-        const float4 x = *reinterpret_cast<const float4 *>(p);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    static __device__ __forceinline__ void open(const uint4 &x, float (&v)[4]) {
+        v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
     }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[4]) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     }
 };
 template <> struct Piece<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[8]) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    static __device__ __forceinline__ void open(const uint4 &x, float (&v)[8]) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -47,147 +46,181 @@ template <> struct Piece<__nv_bfloat16> {
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                   pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+        return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     }
 };
 
-// Item j (0 <= j < rot / (2 Piece::N)) of a rotated block: two 16-byte pieces,
-// either neighbours (interleaved) or half a block apart.
+// An item is two 16-byte pieces: the two that hold P pairs of a rotated block
+// (neighbours if interleaved, else half a block apart), or two to be copied.
 template <typename T>
-__device__ __forceinline__ void rotate_item(const T *x, T *y, const float2 *cs, int j, int rot,
-                                            bool interleaved) {
-    constexpr int P = Piece<T>::N;
-    float a[P], b[P], u[P], v[P];
-    const int ia = interleaved ? 2 * P * j : P * j;
-    const int ib = interleaved ? ia + P : ia + rot / 2;
-    Piece<T>::load(x + ia, a);
-    Piece<T>::load(x + ib, b);
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < P / 2; ++i) {
-            const float2 c = cs[P * j + i], d = cs[P * j + P / 2 + i];
-            u[2 * i] = a[2 * i] * c.x - a[2 * i + 1] * c.y;
-            u[2 * i + 1] = a[2 * i] * c.y + a[2 * i + 1] * c.x;
-            v[2 * i] = b[2 * i] * d.x - b[2 * i + 1] * d.y;
-            v[2 * i + 1] = b[2 * i] * d.y + b[2 * i + 1] * d.x;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float2 c = cs[P * j + i];
-            u[i] = a[i] * c.x - b[i] * c.y;
-            v[i] = a[i] * c.y + b[i] * c.x;
-        }
+struct Item {
+    const T *x0, *x1;            // x1 null: no second piece
+    T *y0, *y1;
+    const float2 *cs;            // of the item's pairs; null: copied
+    // item j of a rotated block of `rot` channels
+    __device__ __forceinline__ void turned(const T *x, T *y, const float2 *table, int j, int rot, bool interleaved) {
+        constexpr int P = Piece<T>::N;
+        const int ia = interleaved ? 2 * P * j : P * j, ib = interleaved ? ia + P : ia + rot / 2;
+        x0 = x + ia; x1 = x + ib; y0 = y + ia; y1 = y + ib;
+        cs = table + P * j;
     }
-    Piece<T>::store(y + ia, u);
-    Piece<T>::store(y + ib, v);
-}
+    // channels [c, c + P) and [d, d + P) (none if d < 0)
+    __device__ __forceinline__ void copied(const T *x, T *y, int c, int d) {
+        x0 = x + c; y0 = y + c;
+        x1 = d < 0 ? nullptr : x + d; y1 = y + d;
+        cs = nullptr;
+    }
+    __device__ __forceinline__ void run(bool interleaved) {
+        constexpr int P = Piece<T>::N;
+        uint4 a = *reinterpret_cast<const uint4 *>(x0), b = make_uint4(0, 0, 0, 0);
+        if (x1) b = *reinterpret_cast<const uint4 *>(x1);
+        if (cs) {
+            float u[P], v[P], p[P], q[P];
+            Piece<T>::open(a, u);
+            Piece<T>::open(b, v);
+            if (interleaved) {
+#pragma unroll
+                for (int i = 0; i < P / 2; ++i) {
+                    const float2 c = cs[i], d = cs[P / 2 + i];
+                    p[2 * i] = u[2 * i] * c.x - u[2 * i + 1] * c.y;
+                    p[2 * i + 1] = u[2 * i] * c.y + u[2 * i + 1] * c.x;
+                    q[2 * i] = v[2 * i] * d.x - v[2 * i + 1] * d.y;
+                    q[2 * i + 1] = v[2 * i] * d.y + v[2 * i + 1] * d.x;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float2 c = cs[i];
+                    p[i] = u[i] * c.x - v[i] * c.y;
+                    q[i] = u[i] * c.y + v[i] * c.x;
+                }
+            }
+            a = Piece<T>::pack(p);
+            b = Piece<T>::pack(q);
+        }
+        *reinterpret_cast<uint4 *>(y0) = a;
+        if (x1) *reinterpret_cast<uint4 *>(y1) = b;
+    }
+};
+
+// e / n with inv = 1.f / n: (e + 1/2) / n lies 1 / (2 n) or more from every whole
+// number, and the product is off by at most 2^-23 of it, so it is exact while
+// (e / n) n < 2^22, i.e. e < 2^22.
+__device__ __forceinline__ int quotient(int e, float inv) { return (int)(((float)e + 0.5f) * inv); }
+
+// Blocks an SM and rounds of a block's threads over its items, for 8192 tokens of
+// 32 heads of 192 channels: six blocks and eight rounds 36.8 us; four rounds 42.6;
+// two or four items of a thread in flight in fewer blocks 37.2 to 46.7.
+constexpr int BLOCKS = 6, ROUNDS = 8;
 
 template <typename T>
-__device__ __forceinline__ void copy_piece(const T *x, T *y) {
-    *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<const uint4 *>(x);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, BLOCKS)
 rope_kernel(const T *x, const int32_t *__restrict__ positions, const float *__restrict__ freqs, T *out,
             long long tokens, int H, int d, int rot, int offset, long long xs, long long os, int tpb,
-            bool interleaved, bool inverse, float scale)
+            int heads, bool interleaved, bool inverse, float scale)
 {
+    // tpb tokens, and `heads` of their heads (blockIdx.y-th share)
     extern __shared__ float2 cs[];                       // [tpb][rot / 2]
     constexpr int P = Piece<T>::N;
     const long long t0 = (long long)blockIdx.x * tpb;
     const int nt = (int)min((long long)tpb, tokens - t0);
+    const int h0 = blockIdx.y * heads, nh = min(heads, H - h0);
     const int half = rot / 2;
     for (int e = threadIdx.x; e < nt * half; e += NT)
         cs[e] = turn(positions[t0 + e / half], freqs[e % half], scale, inverse);
     __syncthreads();
-    // items of a head: the rotated pairs of pieces, then (out of place) the other pieces
-    const int nrot = rot / (2 * P);
-    const int per = nrot + (x == out ? 0 : (d - rot) / P);
-    const int all = nt * H * per;
+    // items of a head: the rotated ones, then (out of place) the other pieces two by two
+    const int nrot = rot / (2 * P), rest = (d - rot) / P;
+    const int per = nrot + (x == out ? 0 : (rest + 1) / 2);
+    const int all = nt * nh * per;
+    const float inv_per = 1.f / per, inv_nh = 1.f / nh;
     for (int e = threadIdx.x; e < all; e += NT) {
-        const int th = e / per, j = e - th * per;
-        const int t = th / H, h = th - t * H;
+        const int th = quotient(e, inv_per), j = e - th * per;
+        const int t = quotient(th, inv_nh), h = h0 + th - t * nh;
         const T *xr = x + (t0 + t) * xs + (long long)h * d;
         T *yr = out + (t0 + t) * os + (long long)h * d;
+        Item<T> it;
         if (j < nrot) {
-            rotate_item<T>(xr + offset, yr + offset, cs + t * half, j, rot, interleaved);
+            it.turned(xr + offset, yr + offset, cs + t * half, j, rot, interleaved);
         } else {
-            const int c = (j - nrot) * P;
-            const int at = c < offset ? c : c + rot;
-            copy_piece<T>(xr + at, yr + at);
+            const int c = 2 * (j - nrot) * P, c2 = c + P;
+            it.copied(xr, yr, c < offset ? c : c + rot, c2 >= rest * P ? -1 : c2 < offset ? c2 : c2 + rot);
         }
+        it.run(interleaved);
     }
 }
 
+constexpr int TPB = 8;          // tokens of an append block at most: one a warp
+
 template <typename T>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, BLOCKS)
 latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int32_t *__restrict__ table,
                      const int32_t *__restrict__ kv_lens, const int32_t *__restrict__ cu,
                      const T *__restrict__ q_pe, T *__restrict__ q, const float *__restrict__ freqs,
                      int tokens, int H, int dk, int rot, int N, int per_seq, int num_pages, int page_size,
                      int max_pages, long long page_stride, long long kvs, long long qts, long long qhs,
-                     bool interleaved, float scale, int *err)
+                     int tpb, bool interleaved, float scale, int *err)
 {
-    // one token a block: its place, its cosines and sines, then its pieces
-    extern __shared__ float2 cs[];                       // [rot / 2]
-    __shared__ int place[2];                             // page (-1: skip), row in it
-    __shared__ int where;                                // position
+    extern __shared__ float2 cs[];                       // [tpb][rot / 2]
+    __shared__ long long place[TPB];                     // offset of the token's cache row, -1: skip
+    __shared__ int where[TPB];                           // its position
     constexpr int P = Piece<T>::N;
-    const int t = blockIdx.x;
-    if (threadIdx.x < 32) {
+    const int t0 = blockIdx.x * tpb, nt = min(tpb, tokens - t0);
+    const int warp = threadIdx.x >> 5;
+    if (warp < nt) {
+        const int t = t0 + warp;
         const int n = paged::sequence_of(cu, N, per_seq, tokens, t);
-        if (threadIdx.x == 0) {
-            int page = -1, pos = 0;
-            if (n < N) {
-                // a token behind the last sequence is no error: it is padding
-                const int b = paged::token_offset(cu, n, per_seq, tokens);
+        if ((threadIdx.x & 31) == 0) {
+            long long row = -1;
+            int pos = 0;
+            const int b = n < N ? paged::token_offset(cu, n, per_seq, tokens) : tokens;
+            if (t >= b) {                                // (else it belongs to no sequence: padding)
                 const int e = paged::token_offset(cu, n + 1, per_seq, tokens);
                 const long long at = (long long)kv_lens[n] - (e - b) + (t - b);
-                if (t < b) page = -2;                    // before the first sequence: padding as well
-                else if (at >= 0 && at < (long long)max_pages * page_size) {
+                int page = -1;
+                if (at >= 0 && at < (long long)max_pages * page_size) {
                     pos = (int)at;
                     page = table[(long long)n * max_pages + pos / page_size];
                 }
-                if (page != -2 && (page < 0 || page >= num_pages)) {
-                    page = -1;
-                    set_device_error(err, paged::kErrBadPage);
-                }
+                if (page >= 0 && page < num_pages) row = page * page_stride + (long long)(pos % page_size) * dk;
+                else set_device_error(err, paged::kErrBadPage);
             }
-            place[0] = page;
-            place[1] = pos % page_size;
-            where = pos;
+            place[warp] = row;
+            where[warp] = pos;
         }
     }
     __syncthreads();
-    if (place[0] < 0) return;
     const int half = rot / 2;
     if (freqs) {
-        for (int i = threadIdx.x; i < half; i += NT) cs[i] = turn(where, freqs[i], scale, false);
+        for (int e = threadIdx.x; e < nt * half; e += NT) cs[e] = turn(where[e / half], freqs[e % half], scale, false);
         __syncthreads();
     }
-    const T *src = kv + t * kvs;
-    T *row = cache + (long long)place[0] * page_stride + (long long)place[1] * dk;
+    // items of a token: its latent (turned at the end, the rest copied), then each head of q
     const int turned = freqs ? rot : 0;
-    const int nrot = turned / (2 * P), ncopy = (dk - turned) / P;
-    // a head of q: its rotary part turned, or copied without positions
-    const int nq = q ? (freqs ? rot / (2 * P) : rot / P) : 0;
-    const int all = nrot + ncopy + nq * H;
+    const int nrot = turned / (2 * P), rest = (dk - turned) / P, nkv = nrot + (rest + 1) / 2;
+    const int nq = q ? rot / (2 * P) : 0;
+    const int per = nkv + nq * H;
+    const int all = nt * per;
+    const float inv_per = 1.f / per, inv_nq = nq ? 1.f / nq : 0.f;
     for (int e = threadIdx.x; e < all; e += NT) {
-        if (e < ncopy) {
-            copy_piece<T>(src + e * P, row + e * P);
-        } else if (e < ncopy + nrot) {
-            rotate_item<T>(src + dk - rot, row + dk - rot, cs, e - ncopy, rot, interleaved);
+        const int t = tpb == 1 ? 0 : quotient(e, inv_per), j = e - t * per;
+        if (place[t] < 0) continue;
+        const float2 *c = cs + t * half;
+        Item<T> it;
+        if (j < nkv) {
+            const T *src = kv + (t0 + t) * kvs;
+            T *row = cache + place[t];
+            if (j < nrot) it.turned(src + dk - rot, row + dk - rot, c, j, rot, interleaved);
+            else it.copied(src, row, 2 * (j - nrot) * P, 2 * (j - nrot) + 1 < rest ? (2 * (j - nrot) + 1) * P : -1);
         } else {
-            const int h = (e - ncopy - nrot) / nq, j = (e - ncopy - nrot) - h * nq;
-            const T *x = q_pe + t * qts + h * qhs;
-            T *y = q + ((long long)t * H + h) * dk + dk - rot;
-            if (freqs) rotate_item<T>(x, y, cs, j, rot, interleaved);
-            else copy_piece<T>(x + j * P, y + j * P);
+            const int h = quotient(j - nkv, inv_nq), i = j - nkv - h * nq;
+            const T *src = q_pe + (t0 + t) * qts + h * qhs;
+            T *row = q + ((long long)(t0 + t) * H + h) * dk + dk - rot;
+            if (freqs) it.turned(src, row, c, i, rot, interleaved);
+            else it.copied(src, row, 2 * i * P, (2 * i + 1) * P);
         }
+        it.run(interleaved);
     }
 }
 
@@ -196,14 +229,23 @@ cudaError_t rope_t(const void *x, const int32_t *positions, const float *freqs, 
                    int H, int d, int rot, int offset, long long xs, long long os, bool interleaved,
                    bool inverse, float scale, cudaStream_t st)
 {
-    // tokens of a block: enough pieces for four rounds of its threads
-    const int pieces = H * (d / Piece<T>::N);
-    int tpb = 4 * NT / (pieces > 0 ? pieces : 1);
-    tpb = tpb < 1 ? 1 : tpb > 16 ? 16 : tpb;
+    // a block: ROUNDS items a thread, from several tokens or from a share of one token's heads
+    constexpr int P = Piece<T>::N;
+    const int per = x == out ? rot / (2 * P) : (d / P + 1) / 2;
+    const int want = ROUNDS * NT;
+    int heads = want / per;
+    heads = heads < 1 ? 1 : heads > H ? H : heads;
+    int shares = (H + heads - 1) / heads;
+    heads = (H + shares - 1) / shares;
+    shares = (H + heads - 1) / heads;
+    int tpb = want / (heads * per);
+    tpb = shares > 1 || tpb < 1 ? 1 : tpb > 16 ? 16 : tpb;
+    // few tokens: no more than a round a block
+    while (tpb > 1 && tokens / tpb < 512) tpb >>= 1;
     const long long blocks = (tokens + tpb - 1) / tpb;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    rope_kernel<T><<<(unsigned)blocks, NT, sizeof(float2) * tpb * (rot / 2), st>>>(
-        (const T *)x, positions, freqs, (T *)out, tokens, H, d, rot, offset, xs, os, tpb, interleaved, inverse,
+    if (blocks > 0x7fffffffLL || shares > 65535) return cudaErrorInvalidValue;
+    rope_kernel<T><<<dim3((unsigned)blocks, shares), NT, sizeof(float2) * tpb * (rot / 2), st>>>(
+        (const T *)x, positions, freqs, (T *)out, tokens, H, d, rot, offset, xs, os, tpb, heads, interleaved, inverse,
         scale);
     return cudaGetLastError();
 }
@@ -213,10 +255,14 @@ cudaError_t append_t(const void *kv, void *cache, const PagedPlan &p, const void
                      int dk, int rot, long long kvs, long long qts, long long qhs, bool interleaved, float scale,
                      int *err, cudaStream_t st)
 {
-    latent_append_kernel<T><<<p.T, NT, sizeof(float2) * (rot / 2), st>>>(
+    // tokens of a block: up to eight (a warp each for their places), while 512 blocks and more are left;
+    // heads so many that quotient() would not be exact get one
+    int tpb = (long long)p.H * dk > (1 << 18) ? 1 : TPB;
+    while (tpb > 1 && p.T / tpb < 512) tpb >>= 1;
+    latent_append_kernel<T><<<(p.T + tpb - 1) / tpb, NT, sizeof(float2) * tpb * (rot / 2), st>>>(
         (const T *)kv, (T *)cache, p.page_table, p.kv_lens, p.cu_seqlens, (const T *)q_pe, (T *)q, freqs, p.T, p.H, dk,
         rot, p.N, p.cu_seqlens ? 1 : p.T / p.N, p.num_pages, p.page_size, p.max_pages, p.page_stride, kvs, qts, qhs,
-        interleaved, scale, err);
+        tpb, interleaved, scale, err);
     return cudaGetLastError();
 }
 

@@ -541,7 +541,8 @@ enum { KDA_ROPE_INTERLEAVED = 16, KDA_ROPE_INVERSE = 32 };
  *   may equal x with the same stride (in place: only the rotated channels are
  *   touched), else they must not overlap.
  * Supported: KDA_BF16 or KDA_F32; rot a multiple of 16, d, offset and strides
- *   multiples of 8, rot <= 1024; pointers 16-byte aligned (positions, freqs 4).
+ *   multiples of 8, rot <= 1024, d <= 65536; pointers 16-byte aligned
+ *   (positions, freqs 4).
  */
 kda_status kda_rope(const void *x, const int32_t *positions, const float *freqs, void *out,
                     long long T, int H, int d, int rot, int offset, long long x_stride,
@@ -564,8 +565,8 @@ kda_status kda_rope(const void *x, const int32_t *positions, const float *freqs,
  *   token at a negative position or without a valid page is not written, nor is
  *   its part of q, and sets the error word (code 5).
  * Supported: KDA_BF16 or KDA_F32; rot a multiple of 16 in [16, 1024] (or 0
- *   without q_pe and freqs), dk and strides multiples of 8; kv, q_pe, q, cache
- *   16-byte aligned.
+ *   without q_pe and freqs), dk and strides multiples of 8, H * dk <= 2^24; kv,
+ *   q_pe, q, cache 16-byte aligned.
  */
 kda_status kda_latent_append(const void *kv, void *cache, const int32_t *page_table,
                              const int32_t *kv_lens, const int32_t *cu_seqlens,
