@@ -154,7 +154,7 @@ rope_kernel(const T *x, const int32_t *__restrict__ positions, const float *__re
 constexpr int TPB = 8;          // tokens of an append block at most: one a warp
 
 template <typename T>
-__global__ void __launch_bounds__(NT, BLOCKS)
+__global__ void __launch_bounds__(NT, 8)
 latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int32_t *__restrict__ table,
                      const int32_t *__restrict__ kv_lens, const int32_t *__restrict__ cu,
                      const T *__restrict__ q_pe, T *__restrict__ q, const float *__restrict__ freqs,
