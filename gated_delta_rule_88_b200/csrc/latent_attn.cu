@@ -38,7 +38,7 @@ using namespace sm100;
 constexpr int KT = 64;                        // keys of a tile
 constexpr float TH = 8.f;                     // growth of a maximum (log2) that is let pass
 #ifndef OVH
-#define OVH 2
+#define OVH 4
 #endif
 constexpr int OV = OVH;                       // what a row tile costs besides its key tiles, in key tiles
 
@@ -309,7 +309,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         return;
     }
 
-    paged::let_next_start();
     // ---- this block's range of the (row tile, key tile) units
     if (warp == 1) {
         for (int i = lane; i < Small::ALL; i += 32) mbar_init(&z.full[0] + i, i < Small::ONE ? 1 : L::SW);
@@ -729,6 +728,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             w.next(a);
         }
         if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; meta[0].w = meta[1].w = 0; }
+        // (earlier, the second kernel's blocks would wait beside the running ones: 76 us instead of 73)
+        paged::let_next_start();
         if (tid == 0) { a.meta[2 * b] = meta[0]; a.meta[2 * b + 1] = meta[1]; }
     }
     __syncwarp();
