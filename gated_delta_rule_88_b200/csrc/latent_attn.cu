@@ -36,7 +36,10 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 64;                        // keys of a tile
-constexpr float TH = 8.f;                     // growth of a maximum (log2) that is let pass
+// The reference m of a row's exponentials is the maximum of its first tile, and
+// is raised only when a later logit lies above it by this many powers of two: bf16
+// and fp32 keep their relative precision up to 2^127, so nothing is lost below that.
+constexpr float TH = 60.f;
 #ifndef OVH
 #define OVH 4
 #endif
@@ -385,15 +388,17 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = true;
         const int rows_box = min(a.page_size, KT);            // rows of a box
         const int lrb = 31 - __clz(rows_box), lps = 31 - __clz(a.page_size);
-        // the page of box `lane` of key tile j (of the walk's sequence)
-        auto page_of = [&](int j, int boxes) {
-            return lane < boxes ? a.table[(long long)w.n * a.max_pages + ((j * KT + lane * rows_box) >> lps)] : 0;
-        };
         auto boxes_of = [&](int j, int end) { return (max(0, min(KT, end - j * KT)) + rows_box - 1) >> lrb; };
+        // Each lane has one box of the tile: stage m, half of its channels, rows of box `box` (and
+        // lanes 0 .. 3 one of the positional piece), and fetches it as soon as its stage is free.
+        const int m = lane >> 3, box = (lane >> 1) & 3, half = lane & 1;
+        auto page_of = [&](int j, int boxes, int bx) {
+            return bx < boxes ? a.table[(long long)w.n * a.max_pages + ((j * KT + bx * rows_box) >> lps)] : 0;
+        };
         for (; w.more() && ok; w.next(a)) {
             const int end = w.s.keys_of(w.i);
             int boxes = boxes_of(w.j0, end);
-            int page = page_of(w.j0, boxes);
+            int page = page_of(w.j0, boxes, box), page_x = PE && lane < 4 ? page_of(w.j0, boxes, lane) : 0;
             ok = segs == 0 || wait_on(&z.q_empty, (segs - 1) & 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (lane == 0) {
@@ -402,52 +407,57 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int p = 0; p < L::NQ; ++p) tma_2d(sm + p * L::QP, &tm_q, 64 * p, row, &z.q_full);
             }
             ++segs;
-            for (int j = w.j0; j < w.j1 && ok; ++j) {
-                // boxes of 64 channels x (part of) one page's rows
-                const int y = (j * KT + lane * rows_box) & (a.page_size - 1);
+            for (int j = w.j0; j < w.j1; ++j) {
                 const uint32_t bytes = (uint32_t)boxes * rows_box * 128;
-                if (PE) {
-                    uint64_t *fb = &z.x_full[tiles & 1];
-                    ok = tiles < 2 || wait_on(&z.x_empty[tiles & 1], ((tiles >> 1) - 1) & 1, abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
-                    __syncwarp();
-                    if (lane < boxes)
-                        prep::tma_load_3d(sm + L::X_OFF + (tiles & 1) * L::HALF + lane * rows_box * 128, &tm_c, DV, y, page, fb);
-                }
-                for (int m = 0; m < L::MT; ++m) {
-                    uint64_t *fb = &z.full[st];
-                    ok = st_use == 0 || wait_on(&z.empty[st], (st_use - 1) & 1, abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(fb, 2 * bytes);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        unsigned char *dst = sm + L::ST_OFF + st * L::STAGE + lane * rows_box * 128;
-                        prep::tma_load_3d(dst, &tm_c, 128 * m, y, page, fb);
-                        prep::tma_load_3d(dst + L::HALF, &tm_c, 128 * m + 64, y, page, fb);
+                int s = st + m, use = st_use;
+                if (s >= L::NS) { s -= L::NS; ++use; }
+                bool todo = m < L::MT && (box < boxes || (lane & 7) == 0), todo_x = PE && lane < max(1, boxes);
+                for (uint32_t tries = 0;; ++tries) {
+                    if (todo_x && (tiles < 2 || mbar_test_wait(&z.x_empty[tiles & 1], ((tiles >> 1) - 1) & 1))) {
+                        uint64_t *fb = &z.x_full[tiles & 1];
+                        if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
+                        if (lane < boxes)
+                            prep::tma_load_3d(sm + L::X_OFF + (tiles & 1) * L::HALF + lane * rows_box * 128, &tm_c, DV,
+                                              (j * KT + lane * rows_box) & (a.page_size - 1), page_x, fb);
+                        todo_x = false;
                     }
-                    if (++st == L::NS) { st = 0; ++st_use; }
+                    if (todo && (use == 0 || mbar_test_wait(&z.empty[s], (use - 1) & 1))) {
+                        uint64_t *fb = &z.full[s];
+                        if ((lane & 7) == 0) mbar_arrive_expect_tx(fb, 2 * bytes);
+                        if (box < boxes)
+                            prep::tma_load_3d(sm + L::ST_OFF + s * L::STAGE + half * L::HALF + box * rows_box * 128, &tm_c,
+                                              128 * m + 64 * half, (j * KT + box * rows_box) & (a.page_size - 1), page, fb);
+                        todo = false;
+                    }
+                    if (!__any_sync(0xffffffffu, todo || todo_x)) break;
+                    ok = tries < (1u << 24) && !*abort_flag;
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (tries > 4096) __nanosleep(32);
                 }
+                // what was issued, for the drain: a stage's use counts once its lanes are through
+                if (!ok) break;
+                st += L::MT;
+                if (st >= L::NS) { st -= L::NS; ++st_use; }
                 ++tiles;
-                if (j + 1 < w.j1) { boxes = boxes_of(j + 1, end); page = page_of(j + 1, boxes); }
+                if (j + 1 < w.j1) {
+                    boxes = boxes_of(j + 1, end);
+                    page = page_of(j + 1, boxes, box);
+                    if (PE && lane < 4) page_x = page_of(j + 1, boxes, lane);
+                }
             }
         }
         if (!ok) {
             if (lane == 0) {
                 set_device_error(a.err, kErrWaitTimeout);
                 *abort_flag = 1;
-                // never leave with copies in flight into this block's shared memory
-                for (int s = 0; s < L::NS; ++s) {
-                    const int uses = st_use + (s < st ? 1 : 0);
-                    if (uses > 0) mbar_wait(&z.full[s], (uses - 1) & 1, 1u << 20);
+                // never leave with copies in flight into this block's shared memory; a tile that was
+                // begun when the wait ran out may have some of its boxes under way
+                for (int s = 0; s < L::NS; ++s)
+                    for (int k = 0; k < 2; ++k) mbar_wait(&z.full[s], k, 1u << 18);
+                for (int k = 0; k < 2; ++k) {
+                    for (int x = 0; PE && x < 2; ++x) mbar_wait(&z.x_full[x], k, 1u << 18);
+                    mbar_wait(&z.q_full, k, 1u << 18);
                 }
-                for (int x = 0; PE && x < 2; ++x) {
-                    // (the last tile may have its positional piece only)
-                    const int uses = (tiles + 1 - x + 1) / 2;
-                    if (uses > 0) mbar_wait(&z.x_full[x], (uses - 1) & 1, 1u << 18);
-                    if (uses > 1) mbar_wait(&z.x_full[x], (uses - 2) & 1, 1u << 18);
-                }
-                if (segs > 0) mbar_wait(&z.q_full, (segs - 1) & 1, 1u << 20);
             }
         }
     } else if (warp == L::SW + 1) {
@@ -588,6 +598,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bad |= pg < 0 || pg >= a.num_pages;
             }
             float m_run = -INFINITY, l[16];
+            constexpr float NONE = -1e30f;           // stands for no reference: whatever a row sees lies above it by more than TH
+            __syncwarp();
+            mine[lane] = NONE;
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < 16; ++c) l[c] = 0.f;
             // Before the block's first tile the loop runs once on whatever TMEM holds, while Q and the
@@ -608,45 +622,58 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int key = j * KT + r;
                 if (j * KT + KT > least) {
                     // some row does not see the whole tile
+                    __syncwarp();
                     mine[lane] = __int_as_float(sees);
                     __syncwarp();
 #pragma unroll
                     for (int c = 0; c < 16; ++c) x[c] = key < __float_as_int(mine_c[c]) ? x[c] * a.sl2 : -INFINITY;
                     __syncwarp();
+                    mine[lane] = m_run == -INFINITY ? NONE : m_run;
+                    __syncwarp();
                 } else {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) x[c] *= a.sl2;
                 }
+                float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) y[c] = x[c];
-                red[qd][lane] = across_lanes<true>(y, lane);
-                if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
-                const float mt = fmaxf(fmaxf(red[0][lane], red[1][lane]), fmaxf(red[2][lane], red[3][lane]));
-                // the reference is raised only when the maximum has outgrown it by 2^TH
-                const bool raise = mt > m_run + TH || (m_run == -INFINITY && mt > -INFINITY);
-                const float f = raise ? exp2f(m_run - mt) : 1.f;
-                if (raise) m_run = mt;
-                const bool any = __any_sync(0xffffffffu, raise) && j > w.j0;
-                mine[lane] = m_run == -INFINITY ? 0.f : m_run;
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 16; ++c) x[c] = prep::ex2_approx(x[c] - mine_c[c]);
-                if (any) {
-                    __syncwarp();
-                    mine[lane] = f;
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) l[c] *= mine_c[c];
-                    for (int m = 0; m < L::MT; ++m) {
-                        float o[32];
-                        tmem_ld32(lanes + L::O_COL + m * R, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] *= mine[c];
-                        tmem_st32(lanes + L::O_COL + m * R, o);
-                    }
-                    tmem_wait_st();
+                for (int c = 0; c < 16; ++c) {
+                    y[c] = x[c] - mine_c[c];
+                    top = fmaxf(top, y[c]);
                 }
+                const bool high = named_bar_or(1 + cg, 128, !ok || top > TH);
+                if (high) {
+                    // a row without a reference yet, or one that has outgrown it: the tile's maxima
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) y[c] = x[c];
+                    red[qd][lane] = across_lanes<true>(y, lane);
+                    if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
+                    const float mt = fmaxf(fmaxf(red[0][lane], red[1][lane]), fmaxf(red[2][lane], red[3][lane]));
+                    const bool raise = mt > m_run + TH || (m_run == -INFINITY && mt > -INFINITY);
+                    const float f = raise ? exp2f(m_run - mt) : 1.f;
+                    if (raise) m_run = mt;
+                    if (j > w.j0) {
+                        mine[lane] = f;
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) l[c] *= mine_c[c];
+                        for (int m = 0; m < L::MT; ++m) {
+                            float o[32];
+                            tmem_ld32(lanes + L::O_COL + m * R, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] *= mine[c];
+                            tmem_st32(lanes + L::O_COL + m * R, o);
+                        }
+                        tmem_wait_st();
+                        __syncwarp();
+                    }
+                    mine[lane] = m_run == -INFINITY ? NONE : m_run;
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) y[c] = x[c] - mine_c[c];
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) x[c] = prep::ex2_approx(y[c]);
                 unsigned char *P = sm + L::P_OFF;
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
@@ -670,6 +697,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (dry) {
                     m_run = -INFINITY;
+                    mine[lane] = NONE;
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < 16; ++c) l[c] = 0.f;
                     continue;
