@@ -411,28 +411,32 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t bytes = (uint32_t)boxes * rows_box * 128;
                 int s = st + m, use = st_use;
                 if (s >= L::NS) { s -= L::NS; ++use; }
-                bool todo = m < L::MT && (box < boxes || (lane & 7) == 0), todo_x = PE && lane < max(1, boxes);
-                for (uint32_t tries = 0;; ++tries) {
-                    if (todo_x && (tiles < 2 || mbar_test_wait(&z.x_empty[tiles & 1], ((tiles >> 1) - 1) & 1))) {
-                        uint64_t *fb = &z.x_full[tiles & 1];
-                        if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
-                        if (lane < boxes)
-                            prep::tma_load_3d(sm + L::X_OFF + (tiles & 1) * L::HALF + lane * rows_box * 128, &tm_c, DV,
-                                              (j * KT + lane * rows_box) & (a.page_size - 1), page_x, fb);
-                        todo_x = false;
-                    }
-                    if (todo && (use == 0 || mbar_test_wait(&z.empty[s], (use - 1) & 1))) {
-                        uint64_t *fb = &z.full[s];
+                bool todo = m < L::MT && (box < boxes || (lane & 7) == 0);
+                if (PE) {
+                    // (a positional piece is free long before the stages are)
+                    uint64_t *eb = tiles < 2 ? nullptr : &z.x_empty[tiles & 1], *fb = &z.x_full[tiles & 1];
+                    if (!(ok = warp_wait(eb, ((tiles >> 1) - 1) & 1, abort_flag))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
+                    if (lane < boxes && lane < 4)
+                        prep::tma_load_3d(sm + L::X_OFF + (tiles & 1) * L::HALF + lane * rows_box * 128, &tm_c, DV,
+                                          (j * KT + lane * rows_box) & (a.page_size - 1), page_x, fb);
+                    __syncwarp();
+                }
+                uint64_t *fb = &z.full[s], *eb = &z.empty[s];
+                const uint32_t parity = (use - 1) & 1;
+                unsigned char *dst = sm + L::ST_OFF + s * L::STAGE + half * L::HALF + box * rows_box * 128;
+                const int x = 128 * m + 64 * half, y = (j * KT + box * rows_box) & (a.page_size - 1);
+                for (uint32_t tries = 1; __any_sync(0xffffffffu, todo); ++tries) {
+                    if (todo && (use == 0 || mbar_test_wait(eb, parity))) {
                         if ((lane & 7) == 0) mbar_arrive_expect_tx(fb, 2 * bytes);
-                        if (box < boxes)
-                            prep::tma_load_3d(sm + L::ST_OFF + s * L::STAGE + half * L::HALF + box * rows_box * 128, &tm_c,
-                                              128 * m + 64 * half, (j * KT + box * rows_box) & (a.page_size - 1), page, fb);
+                        if (box < boxes) prep::tma_load_3d(dst, &tm_c, x, y, page, fb);
                         todo = false;
                     }
-                    if (!__any_sync(0xffffffffu, todo || todo_x)) break;
-                    ok = tries < (1u << 24) && !*abort_flag;
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    if (tries > 4096) __nanosleep(32);
+                    if ((tries & 63) == 0) {
+                        ok = tries < (1u << 24) && !*abort_flag;
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        __nanosleep(32);
+                    }
                 }
                 // what was issued, for the drain: a stage's use counts once its lanes are through
                 if (!ok) break;
@@ -508,11 +512,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
 #pragma unroll
                 for (int m = 0; m < L::MT; ++m) {
-                    if (ok && !all) {
-                        ok = __all_sync(0xffffffffu, wait_on(&z.full[st], st_use & 1, abort_flag));
-                        tc_fence_after();
-                    }
                     const uint32_t k_lo = k_d.lo + (uniform_of(st) * L::STAGE >> 4), q_lo = q_d.lo + (2 * m * L::QP >> 4);
+                    if (ok && !all) ok = __all_sync(0xffffffffu, wait_on(&z.full[st], st_use & 1, abort_flag));
                     if (ok && elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
