@@ -592,9 +592,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int end = w.s.keys_of(w.i);
             const int sees = lane < rows ? w.s.sees(w.i * R + 32 * cg + lane) : 0;
             const int least = __reduce_min_sync(0xffffffffu, lane < rows ? sees : 0x7fffffff);
-            // the sequence's pages, all of them: every block that has a piece of it comes to the same answer
+            // the segment's pages (one of a split tile's pieces with a bad page spoils all of it)
             bool bad = false;
-            for (int p = t; (long long)p * a.page_size < w.s.kv; p += 128) {
+            const int lps = 31 - __clz(a.page_size), stop = min(w.j1 * KT, end);
+            for (int p = (w.j0 * KT >> lps) + t; p << lps < stop; p += 128) {
                 const int pg = a.table[(long long)w.n * a.max_pages + p];
                 bad |= pg < 0 || pg >= a.num_pages;
             }
@@ -722,16 +723,15 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (a.lse && qd == 0 && lane < rows && !bad)
                     a.lse[row0 + 32 * cg + lane] = sum > 0.f ? (m_run + log2f(sum)) * 0.693147180559945f : -INFINITY;
                 __syncwarp();
-                if (!bad)
-                    for (int m = 0; m < L::MT; ++m) {
-                        float o[32];
-                        tmem_ld32(lanes + L::O_COL + m * R, o);
-                        tmem_wait_ld();
-                        __nv_bfloat16 *dst = a.out + (row0 + 32 * cg) * DV + 128 * m + t;
+                for (int m = 0; m < L::MT; ++m) {
+                    float o[32];
+                    tmem_ld32(lanes + L::O_COL + m * R, o);
+                    tmem_wait_ld();
+                    __nv_bfloat16 *dst = a.out + (row0 + 32 * cg) * DV + 128 * m + t;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c < rows) dst[(size_t)c * DV] = __float2bfloat16_rn(o[c] * mine[c]);
-                    }
+                    for (int c = 0; c < 32; ++c)
+                        if (c < rows && !bad) dst[(size_t)c * DV] = __float2bfloat16_rn(o[c] * mine[c]);
+                }
             } else {
                 // a piece: slot 0 if it continues the row tile, slot 1 if it begins it
                 const size_t at = (size_t)(2 * b + (w.j0 == 0 ? 1 : 0)) * R + 32 * cg;
@@ -742,7 +742,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_wait_ld();
                     float *dst = a.ws_o + at * DV + 128 * m + t;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) dst[(size_t)c * DV] = o[c];
+                    for (int c = 0; c < 32; ++c)
+                        if (c < rows) dst[(size_t)c * DV] = o[c];
                 }
                 if (tid == 0) {
                     // the blocks of its first and last key tile; unit u is in block (u G + G - 1) / total

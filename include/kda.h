@@ -485,9 +485,11 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  *               read nor written), or NULL: T / num_seqs tokens each.
  * New token i of a sequence with L of them sits at position kv_len - L + i.
  * All index arrays are device int32, 4-byte aligned, and read on the device.
- * A sequence with kv_len < 0, kv_len > max_pages * page_size, or (where the
- * call reads it) a page outside [0, num_pages) sets the device error word
- * (kda_get_device_error: code 5); its outputs are not written.
+ * A sequence with kv_len < 0 or kv_len > max_pages * page_size, or a page
+ * outside [0, num_pages) that holds a key or takes a token, sets the device error
+ * word (kda_get_device_error: code 5).  The outputs of such a sequence, or of the
+ * tokens that would have used such a page, are not written (nor need those of the
+ * same sequence's other tokens be).
  * page_size: 16, 32, 64 or 128.
  * ---------------------------------------------------------------------------
  */
