@@ -49,7 +49,7 @@ kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page
     kda_status s = check_plan(fn, p, dk, dtype);
     if (s != KDA_OK) return s;
     if (flags & ~(unsigned)KDA_ATTN_FULL) return fail(KDA_ERR_INVALID_ARG, "%s: unknown flag bits 0x%x", fn, flags);
-    if (!finite_f(scale)) return fail(KDA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (!finite_f(scale * 1.4426951f)) return fail(KDA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
     if (!aligned16(q) || !aligned16(cache) || !aligned16(out))
         return fail(KDA_ERR_INVALID_ARG, "%s: q, cache and out must be 16-byte aligned", fn);
     if (!aligned4(lse)) return fail(KDA_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", fn);

@@ -491,6 +491,9 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * tokens that would have used such a page, are not written (nor need those of the
  * same sequence's other tokens be).
  * page_size: 16, 32, 64 or 128.
+ * Make the first call of each of these entry points on a device before any
+ * stream capture there; after that they may be captured, and two captured calls
+ * may run at once (each has a workspace of its own).
  * ---------------------------------------------------------------------------
  */
 
@@ -507,7 +510,8 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * kv_len < L and i < L - kv_len) gets out = 0, lse = -inf.
  * Layout: q [T, H, dk] dtype; out [T, H, dv] dtype; lse [T, H] float32 or NULL.
  * Cache rows at positions >= kv_len are never used and may hold anything;
- *   rows below it must be finite.
+ *   rows below it must be finite, as must q (of the tokens that count) and the
+ *   logits x_j, above -1e30.
  * Deterministic: the same call gives the same bits.
  * Memory: a stream-ordered workspace from the library's pool, of a size that
  *   depends on the device, H, T / num_seqs and dv only (at most 39 MB).

@@ -50,7 +50,7 @@ NAN, INF = float("nan"), float("inf")
 @pytest.mark.parametrize("kw", [
     dict(q=0), dict(cache=0), dict(table=0), dict(lens=0), dict(out=0), dict(T=-1), dict(H=0), dict(dk=0), dict(N=0),
     dict(pages=0), dict(mp=0), dict(T=5), dict(N=65536, T=65536), dict(H=65536), dict(dtype=2), dict(flags=1),
-    dict(flags=16), dict(scale=NAN), dict(scale=INF), dict(q=FAKE + 8), dict(cache=FAKE + 8), dict(out=FAKE + 4),
+    dict(flags=16), dict(scale=NAN), dict(scale=INF), dict(scale=3e38), dict(q=FAKE + 8), dict(cache=FAKE + 8), dict(out=FAKE + 4),
     dict(lse=FAKE + 2), dict(table=FAKE + 1), dict(lens=FAKE + 2), dict(cu=FAKE + 2), dict(ps=64 * 576 - 8),
     dict(ps=64 * 576 + 4), dict(ps=-8), dict(mp=1 << 26), dict(T=1 << 30, H=4, N=1)])
 def test_attn_bad_arguments_rejected(lib, kw):
@@ -74,7 +74,8 @@ def test_attn_no_tokens_is_a_no_op(lib):
     dict(N=0), dict(T=5), dict(rot=24), dict(rot=-16), dict(rot=592), dict(rot=0), dict(rot=1040, dk=2048),
     dict(dk=580), dict(kvs=568), dict(kvs=580), dict(ts=100), dict(hs=60), dict(hs=72 + 4), dict(ts=32), dict(hs=32),
     dict(flags=32), dict(flags=1), dict(scale=INF), dict(scale=NAN), dict(dtype=-1), dict(kv=FAKE + 2),
-    dict(cache=FAKE + 8), dict(q_pe=FAKE + 4), dict(q=FAKE + 8), dict(freqs=FAKE + 2), dict(ps=8), dict(ps=4)])
+    dict(cache=FAKE + 8), dict(q_pe=FAKE + 4), dict(q=FAKE + 8), dict(freqs=FAKE + 2), dict(ps=8), dict(ps=4),
+    dict(H=60000)])
 def test_append_bad_arguments_rejected(lib, kw):
     assert append(lib, **kw) == 1
     assert b"kda_latent_append" in lib.kda_last_error_message()
@@ -91,7 +92,8 @@ def test_append_unsupported_and_empty(lib):
     dict(rot=24), dict(rot=144, d=128), dict(offset=72), dict(offset=-8), dict(offset=4), dict(d=100, offset=0),
     dict(rot=1040, d=2048, offset=0), dict(xs=128), dict(os=128), dict(xs=260), dict(os=-256), dict(flags=8),
     dict(flags=64), dict(scale=NAN), dict(dtype=3), dict(x=FAKE + 8), dict(out=FAKE + 2), dict(pos=FAKE + 2),
-    dict(freqs=FAKE + 1), dict(xs=512), dict(H=1 << 24, d=128)])
+    dict(freqs=FAKE + 1), dict(xs=512), dict(H=1 << 24, d=128),
+    dict(d=65544, offset=0)])
 def test_rope_bad_arguments_rejected(lib, kw):
     assert rope(lib, **kw) == 1
     assert b"kda_rope" in lib.kda_last_error_message()

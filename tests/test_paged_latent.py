@@ -327,6 +327,76 @@ def test_attn_lengths_may_change_under_a_graph():
         check_attn(out, lse, oracle(q, [k[:n] for k, n in zip(c.keys, now)], [1, 1], 512, 0.07))
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_attn_random_shapes_match(seed):
+    g = gen(500 + seed)
+    pick = lambda *v: v[int(torch.randint(0, len(v), (1,), generator=g))]
+    N, H, page = pick(1, 2, 5), pick(1, 4, 12, 20, 32, 40, 64, 96), pick(16, 32, 64, 128)
+    dv, dr = pick((512, 64), (512, 64), (512, 0), (256, 64), (256, 0))
+    counts = torch.randint(0, pick(2, 4, 20) + 1, (N,), generator=g).tolist()
+    counts[0] = max(1, counts[0])
+    lens = torch.randint(0, pick(3, 70, 600, 1500), (N,), generator=g).tolist()
+    causal = pick(True, True, False)
+    c = Cache(lens, page, dv + dr, seed=seed, poison=pick(float("nan"), 1e30), gap=pick(0, 8, 64 * 576))
+    q, out, lse, scale = run_attn(c, counts, H, dv, seed=seed, causal=causal, varlen=True, qscale=pick(1.0, 1.0, 8.0))
+    assert kda.kda_get_device_error() == 0
+    check_attn(out, lse, oracle(q, c.keys, counts, dv, scale, causal))
+
+
+def test_attn_many_short_sequences():
+    """More sequences than threads, some without tokens, some without keys."""
+    g = gen(41)
+    N = 1500
+    lens = torch.randint(0, 4, (N,), generator=g).tolist()
+    counts = torch.randint(0, 3, (N,), generator=g).tolist()
+    c = Cache(lens, 16, 576, seed=41)
+    q, out, lse, scale = run_attn(c, counts, 2, 512)
+    assert kda.kda_get_device_error() == 0
+    check_attn(out, lse, oracle(q, c.keys, counts, 512, scale))
+
+
+def test_attn_long_sequence_in_many_pieces():
+    """One sequence over every SM, and a bad page in the middle of it: nothing
+    of the split tile is written."""
+    n = 70000
+    keys = torch.randn(n, 576, generator=gen(42)).to(torch.bfloat16)
+    pages = -(-n // 16)
+    cache = torch.zeros(pages * 16, 576, dtype=torch.bfloat16)
+    cache[:n] = keys
+    order = torch.randperm(pages, generator=gen(43))
+    shuffled = torch.empty_like(cache).view(pages, 16, 576)
+    shuffled[order] = cache.view(pages, 16, 576)
+    dev, table = shuffled.to(DEV), order.int()[None].to(DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = torch.randn(2, 8, 576, generator=gen(44)).to(torch.bfloat16)
+    out, lse = kda.kda_latent_attn(q.to(DEV), dev, table, lens, scale=0.07)
+    assert kda.kda_get_device_error() == 0
+    check_attn(out, lse, oracle(q, [keys], [2], 512, 0.07))
+    table[0, 2500] = -3
+    out.fill_(7)
+    lse.fill_(7)
+    kda.kda_latent_attn(q.to(DEV), dev, table, lens, out=out, lse=lse, scale=0.07)
+    assert kda.kda_get_device_error() == 5
+    assert (out == 7).all() and (lse == 7).all()
+
+
+def test_attn_two_streams_at_once():
+    cases = []
+    for seed, lens, counts in ((51, [4000, 300], [1, 1]), (52, [900, 2500], [6, 6])):
+        c = Cache(lens, 64, 576, seed=seed)
+        q, out, lse, scale = run_attn(c, counts, 32, 512, seed=seed)
+        cases.append((torch.cuda.Stream(), q.to(DEV), *c.to_gpu(), scale, out, lse, []))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for stream, q, cache, table, lens, scale, _, _, got in cases:
+            with torch.cuda.stream(stream):
+                got.append(kda.kda_latent_attn(q, cache, table, lens, scale=scale))
+    torch.cuda.synchronize()
+    assert kda.kda_get_device_error() == 0
+    for *_, out, lse, got in cases:
+        assert all(torch.equal(o, out) and torch.equal(s, lse) for o, s in got)
+
+
 # ------------------------------------------------------------------ rotary positions
 def rotate64(x, pos, freqs, interleaved, inverse=False, scale=1.0):
     """x [T,H,rot] in 64 bits."""
