@@ -40,10 +40,19 @@ constexpr int KT = 64;                        // keys of a tile
 // is raised only when a later logit lies above it by this many powers of two: bf16
 // and fp32 keep their relative precision up to 2^127, so nothing is lost below that.
 constexpr float TH = 60.f;
-#ifndef OVH
-#define OVH 4
-#endif
-constexpr int OV = OVH;                       // what a row tile costs besides its key tiles, in key tiles
+// What a row tile costs besides its key tiles, in key tiles: 32 sequences x 4 tokens
+// up to 8000 keys take 101 us with 0, 93.7 with 1, 88 with 2, 84.6 with 4, 87.8 with 8;
+// 64 sequences x 1 token 77.7, 76.6, 73, 72 and 75.
+constexpr int OV = 4;
+// What splitting costs a block, in key tiles (pieces written and joined): at 64
+// sequences x 4 tokens of 512 keys (8 tiles) 40.1 us split and 30.8 whole, at one
+// sequence of 300 keys 13.5 split and 18.5 whole; 8 picks the better of both in 108 of
+// 114 shapes of 1 to 200 sequences and 128 to 4096 keys, 6 and 10 in fewer.
+constexpr int SPLIT_COST = 8;
+// Up to this many key tiles a sequence nothing is split, and the second kernel is not
+// even launched: one sequence of 128 keys 10.8 us instead of 11.8 (of 300 keys 16.8
+// instead of 13.5).
+constexpr int WHOLE_TILES = 4;
 
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((mn ? 1u : 0u) << 15) | ((mn ? 1u : 0u) << 16) |
@@ -88,6 +97,7 @@ struct Small {
     uint64_t full[12], empty[12], x_full[2], x_empty[2], q_full, q_empty, s_full[2], o_full, drain[2], s_free[2], p_full;
     static constexpr int ONE = 35, ALL = 38;
     long long scan[12];
+    int scan_rt[12], scan_max[12];
     long long start_u;           // first unit of the block's row tile, counted over all
     int start[6];                // sequence, its first token, new tokens, keys; row tile; unit in it
     uint32_t tmem;
@@ -105,7 +115,7 @@ struct Args {
     int4 *meta;                  // [2 * blocks]: a split row tile: first row, rows, first block, pieces
     int T, H, N, per, num_pages, page_size, max_pages;
     float sl2;                   // scale * log2 e
-    bool full;
+    bool full, split;            // split: there is a workspace, row tiles may be split
     int *err;
 };
 
@@ -184,9 +194,11 @@ template <int R>
 struct Walk {
     Seq<R> s;
     int n, i, j0, j1, tiles, at;                // at: the unit of the row tile that the range goes on with
-    long long left;                             // units of the range from there on
-    __device__ __forceinline__ void start(const Args &a, const Small &sm, long long left_) {
+    long long left;                             // units of the range from there on, or row tiles if whole
+    bool whole;                                 // row tiles are not split
+    __device__ __forceinline__ void start(const Args &a, const Small &sm, long long left_, bool whole_) {
         left = left_;
+        whole = whole_;
         j0 = j1 = 0;
         if (left <= 0) return;
         n = sm.start[0]; i = sm.start[4]; at = sm.start[5];
@@ -195,6 +207,7 @@ struct Walk {
     }
     __device__ __forceinline__ void settle() {
         tiles = s.tiles_of(i);
+        if (whole) { j0 = 0; j1 = tiles; return; }
         const int take = (int)min((long long)(tiles + OV - at), left);
         j0 = max(0, at - OV);
         j1 = max(0, at + take - OV);
@@ -202,7 +215,7 @@ struct Walk {
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next(const Args &a) {
-        left -= min((long long)(tiles + OV - at), left);
+        left -= whole ? 1 : min((long long)(tiles + OV - at), left);
         if (left <= 0) return;
         at = 0;
         ++i;
@@ -308,7 +321,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile int *abort_flag = &z.abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(sm) & 1023) {                  // the swizzled tiles need it; the same for every block
-        if (tid == 0) { set_device_error(a.err, kErrWaitTimeout); a.meta[2 * blockIdx.x].w = a.meta[2 * blockIdx.x + 1].w = 0; }
+        if (tid == 0) set_device_error(a.err, kErrWaitTimeout);
+        if (tid < 2 && a.split) a.meta[2 * blockIdx.x + tid].w = 0;
         return;
     }
 
@@ -323,7 +337,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     const int per = a.N <= L::NT ? 1 : (a.N + L::NT - 1) / L::NT;
     const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
-    long long mysum = 0;
+    long long mysum = 0;                        // units
+    int mytiles = 0, mymax = 0;                 // row tiles, and the most key tiles of one
     Seq<R> s0;                                  // the thread's first sequence
     for (int n = n0; n < n1; ++n) {
         Seq<R> s;
@@ -331,25 +346,40 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (s.bad && blockIdx.x == 0) set_device_error(a.err, paged::kErrBadPage);
         if (n == n0) s0 = s;
         mysum += s.units();
+        const int nt = s.row_tiles();
+        mytiles += nt;
+        if (nt > 0) mymax = max(mymax, s.tiles_of(nt - 1));
     }
     long long incl = mysum;
+    int incl_rt = mytiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+        const int y = __shfl_up_sync(0xffffffffu, incl_rt, o);
+        if (lane >= o) { incl += x; incl_rt += y; }
     }
-    if (lane == 31) z.scan[warp] = incl;
+    mymax = __reduce_max_sync(0xffffffffu, mymax);
+    if (lane == 31) { z.scan[warp] = incl; z.scan_rt[warp] = incl_rt; z.scan_max[warp] = mymax; }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = z.tmem;
     long long before = incl - mysum, total = 0;
+    int before_rt = incl_rt - mytiles, total_rt = 0;
 #pragma unroll
     for (int w = 0; w < L::NT / 32; ++w) {
         const long long x = z.scan[w];
-        if (w < warp) before += x;
+        const int y = z.scan_rt[w];
+        if (w < warp) { before += x; before_rt += y; }
         total += x;
+        total_rt += y;
+        mymax = max(mymax, z.scan_max[w]);
     }
+    // Row tiles stay whole where that costs no more: the fullest block's key tiles against an
+    // equal share of all and SPLIT_COST for writing the pieces and joining them.
+    const long long rounds = (total_rt + (int)gridDim.x - 1) / (int)gridDim.x;
+    const bool whole = !a.split || (rounds * (mymax + OV) - SPLIT_COST) * gridDim.x <= total;
+    if (whole) { total = total_rt; before = before_rt; mysum = mytiles; }
     // as many ranges as blocks, but none empty: the pieces of a row tile lie in consecutive blocks
     const int G = total < (long long)gridDim.x ? max(1, (int)total) : (int)gridDim.x;
     const int b = blockIdx.x;
@@ -373,14 +403,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         long long u = u0 - before;
         Seq<R> s = s0;
         int n = n0;
-        for (long long here; n + 1 < n1 && u >= (here = s.units()); s.load(a, ++n)) u -= here;
-        int i, at;
-        s.find(u, i, at);
+        for (long long here; n + 1 < n1 && u >= (here = whole ? s.row_tiles() : s.units()); s.load(a, ++n)) u -= here;
+        int i = (int)u, at = 0;
+        if (!whole) s.find(u, i, at);
         z.start[0] = n; z.start[1] = s.first; z.start[2] = s.L; z.start[3] = s.kv; z.start[4] = i; z.start[5] = at;
     }
     __syncthreads();
     Walk<R> w;
-    w.start(a, z, u1 - u0);
+    w.start(a, z, u1 - u0, whole);
 
     if (warp == L::SW) {
         // ---------------- TMA: Q of each segment, then its key tiles ----------------
@@ -761,7 +791,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!ok) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; meta[0].w = meta[1].w = 0; }
         // (earlier, the second kernel's blocks would wait beside the running ones: 76 us instead of 73)
         paged::let_next_start();
-        if (tid == 0) { a.meta[2 * b] = meta[0]; a.meta[2 * b + 1] = meta[1]; }
+        if (tid == 0 && a.split) { a.meta[2 * b] = meta[0]; a.meta[2 * b + 1] = meta[1]; }
     }
     __syncwarp();
     tc_fence_before();
@@ -774,18 +804,24 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 //     out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,   lse from M and the sum.
 // The rows of a split tile are shared out over the blocks whose ranges it lies
 // in (block x has up to two such tiles: one that it continues, one that it
-// begins), and over gridDim.y.  With few pieces a warp takes a row; with many
-// the block's warps share a row's pieces and add their parts up in order.
+// begins).  With few pieces a warp takes a row; with many the block's warps share
+// a row's pieces and add their parts up in order, and gridDim.y its channels.
 constexpr int CW = 8;                          // warps
+constexpr int CY = 4;                          // gridDim.y
 constexpr int FEW = 8;                         // pieces that one warp takes
+
+// acc += f y
+__device__ __forceinline__ void add_scaled(float4 &acc, float f, const float4 &y) {
+    acc.x = fmaf(f, y.x, acc.x); acc.y = fmaf(f, y.y, acc.y);
+    acc.z = fmaf(f, y.z, acc.z); acc.w = fmaf(f, y.w, acc.w);
+}
 
 template <int R, int DV>
 __global__ void __launch_bounds__(32 * CW)
-latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta,
-                      __nv_bfloat16 *out, float *lse)
+latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta, __nv_bfloat16 *out, float *lse)
 {
-    constexpr int V = DV / 128;                // float4's of a lane
-    __shared__ float4 part[CW][DV / 4];
+    constexpr int V = DV / 128;                // float4's of a row for each lane
+    __shared__ float4 part[CW][32];
     __shared__ float part_l[CW];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     paged::wait_for_previous();
@@ -795,21 +831,19 @@ latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta,
         const int pieces = mt.w, k0 = blockIdx.x - mt.z;
         const bool few = pieces <= FEW;
         auto at = [&](int k, int r) { return (size_t)(k == 0 ? 2 * mt.z + 1 : 2 * (mt.z + k)) * R + r; };
-        // rows k0, k0 + pieces, ...
-        const int step = pieces * gridDim.y * (few ? CW : 1);
-        for (int r = k0 + pieces * (blockIdx.y * (few ? CW : 1) + (few ? warp : 0)); r < mt.y; r += step) {
-            // the first piece of this warp is asked for before the maxima are there
-            const int kf = few ? 0 : warp, kstep = few ? 1 : CW;
-            float4 next[V];
-            if (kf < pieces) {
-                const float4 *o = reinterpret_cast<const float4 *>(ws_o + at(kf, r) * DV) + lane;
+        // rows k0, k0 + pieces, ...: shared out over the warps of all y, or every y has its channels of each
+        const int step = pieces * (few ? CY * CW : 1);
+        for (int r = k0 + (few ? pieces * (blockIdx.y * CW + warp) : 0); r < mt.y; r += step) {
+            auto values = [&](int k) { return reinterpret_cast<const float4 *>(ws_o + at(k, r) * DV) + lane; };
+            auto ml = [&](int k) { return *reinterpret_cast<const float2 *>(ws_ml + at(k, r) * 2); };
+            float4 first[2][V];                 // the first two pieces (there are two) are asked for before the maxima
+            if (few)
 #pragma unroll
-                for (int v = 0; v < V; ++v) next[v] = o[32 * v];
-            }
+                for (int v = 0; v < V; ++v) { first[0][v] = values(0)[32 * v]; first[1][v] = values(1)[32 * v]; }
             float M = -INFINITY;
             bool bad = false;
             for (int k = lane; k < pieces; k += 32) {
-                const float2 x = *reinterpret_cast<const float2 *>(ws_ml + at(k, r) * 2);
+                const float2 x = ml(k);
                 M = fmaxf(M, x.x);
                 bad |= x.y < 0.f;
             }
@@ -817,51 +851,49 @@ latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta,
             for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             if (__any_sync(0xffffffffu, bad)) continue;                  // (the same in all warps)
             const float ref = M == -INFINITY ? 0.f : M;
-            float4 acc[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const size_t row = (size_t)mt.x + r;
             float l = 0.f;
-            for (int k = kf; k < pieces; k += kstep) {
-                const float2 x = *reinterpret_cast<const float2 *>(ws_ml + at(k, r) * 2);
-                float4 y[V];
+            if (few) {
+                float4 acc[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) y[v] = next[v];
-                if (k + kstep < pieces) {
-                    const float4 *o = reinterpret_cast<const float4 *>(ws_o + at(k + kstep, r) * DV) + lane;
+                for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < pieces; ++k) {
+                    const float2 x = ml(k);
+                    const float f = exp2f(x.x - ref);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) next[v] = o[32 * v];
+                    for (int v = 0; v < V; ++v) add_scaled(acc[v], f, k == 0 ? first[0][v] : k == 1 ? first[1][v] : values(k)[32 * v]);
+                    l = fmaf(f, x.y, l);
                 }
-                const float f = exp2f(x.x - ref);
+                const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    acc[v].x = fmaf(f, y[v].x, acc[v].x); acc[v].y = fmaf(f, y[v].y, acc[v].y);
-                    acc[v].z = fmaf(f, y[v].z, acc[v].z); acc[v].w = fmaf(f, y[v].w, acc[v].w);
+                for (int v = 0; v < V; ++v)
+                    reinterpret_cast<uint2 *>(out + row * DV)[32 * v + lane] =
+                        make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv), pack_bf16(acc[v].z * inv, acc[v].w * inv));
+            } else {
+                if (blockIdx.y >= V) break;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int k = warp; k < pieces; k += CW) {
+                    const float2 x = ml(k);
+                    const float f = exp2f(x.x - ref);
+                    add_scaled(acc, f, values(k)[32 * blockIdx.y]);
+                    l = fmaf(f, x.y, l);
                 }
-                l = fmaf(f, x.y, l);
-            }
-            if (!few) {
                 __syncthreads();
-#pragma unroll
-                for (int v = 0; v < V; ++v) part[warp][32 * v + lane] = acc[v];
+                part[warp][lane] = acc;
                 if (lane == 0) part_l[warp] = l;
                 __syncthreads();
                 if (warp != 0) continue;
                 for (int k = 1; k < CW; ++k) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float4 y = part[k][32 * v + lane];
-                        acc[v].x += y.x; acc[v].y += y.y; acc[v].z += y.z; acc[v].w += y.w;
-                    }
+                    add_scaled(acc, 1.f, part[k][lane]);
                     l += part_l[k];
                 }
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                reinterpret_cast<uint2 *>(out + row * DV)[32 * blockIdx.y + lane] =
+                    make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const size_t row = (size_t)mt.x + r;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                reinterpret_cast<uint2 *>(out + row * DV)[32 * v + lane] =
-                    make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv), pack_bf16(acc[v].z * inv, acc[v].w * inv));
-            if (lane == 0 && lse) lse[row] = l > 0.f ? (M + log2f(l)) * 0.693147180559945f : -INFINITY;
+            if (lane == 0 && lse && (few || blockIdx.y == 0))
+                lse[row] = l > 0.f ? (M + log2f(l)) * 0.693147180559945f : -INFINITY;
         }
     }
 }
@@ -898,19 +930,20 @@ cudaError_t launch_t(const void *q, const void *cache, const PagedPlan &p, void 
     a.out = (__nv_bfloat16 *)out;
     a.lse = lse;
     a.ws_o = (float *)ws;
-    a.ws_ml = a.ws_o + (size_t)2 * sms * R * DV;
-    a.meta = (int4 *)(a.ws_ml + (size_t)2 * sms * R * 2);
+    a.ws_ml = ws ? a.ws_o + (size_t)2 * sms * R * DV : nullptr;
+    a.meta = ws ? (int4 *)(a.ws_ml + (size_t)2 * sms * R * 2) : nullptr;
     a.T = p.T; a.H = p.H; a.N = p.N; a.per = p.cu_seqlens ? 1 : p.T / p.N;
     a.num_pages = p.num_pages; a.page_size = p.page_size; a.max_pages = p.max_pages;
     a.sl2 = scale * 1.44269504088896f;
     a.full = full;
+    a.split = ws != nullptr;
     a.err = err;
     const size_t smem = L::MISC + L::SMALL;
     e = cudaFuncSetAttribute(latent_attn_kernel<R, DV, PE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     latent_attn_kernel<R, DV, PE><<<sms, L::NT, smem, st>>>(mq, mc, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return paged::launch_after(latent_combine_kernel<R, DV>, dim3(sms, 4), dim3(32 * CW), 0, st, a.ws_o, a.ws_ml, a.meta,
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.split) return e;
+    return paged::launch_after(latent_combine_kernel<R, DV>, dim3(sms, CY), dim3(32 * CW), 0, st, a.ws_o, a.ws_ml, a.meta,
                                a.out, lse);
 }
 
@@ -920,6 +953,7 @@ int rows_of_tile(const PagedPlan &p) { return (long long)p.T * p.H <= 32LL * p.N
 }  // namespace
 
 size_t latent_attn_workspace(const PagedPlan &p, int dv, int sms) {
+    if ((long long)p.max_pages * p.page_size <= WHOLE_TILES * KT) return 0;
     const size_t R = rows_of_tile(p);
     return 2 * (size_t)sms * (R * (dv + 2) * sizeof(float) + sizeof(int4));
 }

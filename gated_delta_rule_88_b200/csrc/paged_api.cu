@@ -63,11 +63,12 @@ kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page
     cudaError_t e = kda::get_pool(&mp, &sms);
     if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn memory pool");
     void *ws = nullptr;
-    e = cudaMallocFromPoolAsync(&ws, kda::latent_attn_workspace(p, dv, sms), mp, st);
-    if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn workspace allocation");
+    const size_t bytes = kda::latent_attn_workspace(p, dv, sms);
+    if (bytes && (e = cudaMallocFromPoolAsync(&ws, bytes, mp, st)) != cudaSuccess)
+        return cuda_fail(e, "kda_latent_attn workspace allocation");
     e = kda::launch_latent_attn(q, cache, p, out, lse, dk, dv, scale, (flags & KDA_ATTN_FULL) != 0, ws, sms,
                                 kda::error_word(), st);
-    cudaError_t e2 = cudaFreeAsync(ws, st);
+    cudaError_t e2 = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
     if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn launch");
     if (e2 != cudaSuccess) return cuda_fail(e2, "kda_latent_attn workspace release");
     return KDA_OK;
