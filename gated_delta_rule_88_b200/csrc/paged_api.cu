@@ -97,7 +97,6 @@ kda_status kda_latent_append(const void *kv, void *cache, const int32_t *page_ta
     if (q_pe_ts == 0) q_pe_ts = (long long)H * q_pe_hs;
     if (kv_stride == 0) kv_stride = dk;
     const long long lim = 1LL << 38;
-    if ((long long)H * dk > (1 << 24)) return fail(KDA_ERR_INVALID_ARG, "%s: H * dk = %lld exceeds 2^24", fn, (long long)H * dk);
     if (dk % 8 || kv_stride % 8 || kv_stride < dk || kv_stride > lim ||
         (q_pe && (q_pe_hs % 8 || q_pe_ts % 8 || q_pe_hs < rot || q_pe_ts < rot || q_pe_hs > lim || q_pe_ts > lim)))
         return fail(KDA_ERR_INVALID_ARG, "%s: dk and the strides must be multiples of 8 that hold a row (dk=%d kv_stride=%lld "

@@ -51,67 +51,97 @@ template <> struct Piece<__nv_bfloat16> {
     }
 };
 
-// An item is two 16-byte pieces: the two that hold P pairs of a rotated block
-// (neighbours if interleaved, else half a block apart), or two to be copied.
-template <typename T>
-struct Item {
-    const T *x0, *x1;            // x1 null: no second piece
-    T *y0, *y1;
-    const float2 *cs;            // of the item's pairs; null: copied
-    // item j of a rotated block of `rot` channels
-    __device__ __forceinline__ void turned(const T *x, T *y, const float2 *table, int j, int rot, bool interleaved) {
-        constexpr int P = Piece<T>::N;
-        const int ia = interleaved ? 2 * P * j : P * j, ib = interleaved ? ia + P : ia + rot / 2;
-        x0 = x + ia; x1 = x + ib; y0 = y + ia; y1 = y + ib;
-        cs = table + P * j;
+// The threads of a group (`self` of `size`) walk over rows of `per` items each,
+// row by row: the next item of a thread is found without a division.
+struct Step {
+    int row, at, drow, dat, per;
+    __device__ __forceinline__ Step(int self, int size, int per_) : per(per_) {
+        row = self / per; at = self - row * per;
+        drow = size / per; dat = size - drow * per;
     }
-    // channels [c, c + P) and [d, d + P) (none if d < 0)
-    __device__ __forceinline__ void copied(const T *x, T *y, int c, int d) {
-        x0 = x + c; y0 = y + c;
-        x1 = d < 0 ? nullptr : x + d; y1 = y + d;
-        cs = nullptr;
-    }
-    __device__ __forceinline__ void run(bool interleaved) {
-        constexpr int P = Piece<T>::N;
-        uint4 a = *reinterpret_cast<const uint4 *>(x0), b = make_uint4(0, 0, 0, 0);
-        if (x1) b = *reinterpret_cast<const uint4 *>(x1);
-        if (cs) {
-            float u[P], v[P], p[P], q[P];
-            Piece<T>::open(a, u);
-            Piece<T>::open(b, v);
-            if (interleaved) {
-#pragma unroll
-                for (int i = 0; i < P / 2; ++i) {
-                    const float2 c = cs[i], d = cs[P / 2 + i];
-                    p[2 * i] = u[2 * i] * c.x - u[2 * i + 1] * c.y;
-                    p[2 * i + 1] = u[2 * i] * c.y + u[2 * i + 1] * c.x;
-                    q[2 * i] = v[2 * i] * d.x - v[2 * i + 1] * d.y;
-                    q[2 * i + 1] = v[2 * i] * d.y + v[2 * i + 1] * d.x;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float2 c = cs[i];
-                    p[i] = u[i] * c.x - v[i] * c.y;
-                    q[i] = u[i] * c.y + v[i] * c.x;
-                }
-            }
-            a = Piece<T>::pack(p);
-            b = Piece<T>::pack(q);
-        }
-        *reinterpret_cast<uint4 *>(y0) = a;
-        if (x1) *reinterpret_cast<uint4 *>(y1) = b;
+    __device__ __forceinline__ void next() {
+        row += drow; at += dat;
+        if (at >= per) { at -= per; ++row; }
     }
 };
 
-// e / n with inv = 1.f / n: (e + 1/2) / n lies 1 / (2 n) or more from every whole
-// number, and the product is off by at most 2^-23 of it, so it is exact while
-// (e / n) n < 2^22, i.e. e < 2^22.
-__device__ __forceinline__ int quotient(int e, float inv) { return (int)(((float)e + 0.5f) * inv); }
+// `rows` rotated blocks, xs / ys elements apart.  An item is the two 16-byte
+// pieces that hold P pairs: neighbours if interleaved, else half a block apart.
+template <typename T>
+__device__ __forceinline__ void turn_rows(const T *x, long long xs, T *y, long long ys, int rows, int rot,
+                                          const float2 *cs, bool interleaved, int self, int size)
+{
+    constexpr int P = Piece<T>::N;
+    for (Step e(self, size, rot / (2 * P)); e.row < rows; e.next()) {
+        const int ia = interleaved ? 2 * P * e.at : P * e.at, ib = interleaved ? ia + P : ia + rot / 2;
+        const T *xr = x + e.row * xs;
+        T *yr = y + e.row * ys;
+        const uint4 a = *reinterpret_cast<const uint4 *>(xr + ia), b = *reinterpret_cast<const uint4 *>(xr + ib);
+        float2 c[P];
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const float4 two = *reinterpret_cast<const float4 *>(cs + P * e.at + i);
+            c[i] = make_float2(two.x, two.y);
+            c[i + 1] = make_float2(two.z, two.w);
+        }
+        float u[P], v[P], p[P], q[P];
+        Piece<T>::open(a, u);
+        Piece<T>::open(b, v);
+        if (interleaved) {
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+                const float2 f = c[i], g = c[P / 2 + i];
+                p[2 * i] = u[2 * i] * f.x - u[2 * i + 1] * f.y;
+                p[2 * i + 1] = u[2 * i] * f.y + u[2 * i + 1] * f.x;
+                q[2 * i] = v[2 * i] * g.x - v[2 * i + 1] * g.y;
+                q[2 * i + 1] = v[2 * i] * g.y + v[2 * i + 1] * g.x;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                p[i] = u[i] * c[i].x - v[i] * c[i].y;
+                q[i] = u[i] * c[i].y + v[i] * c[i].x;
+            }
+        }
+        *reinterpret_cast<uint4 *>(yr + ia) = Piece<T>::pack(p);
+        *reinterpret_cast<uint4 *>(yr + ib) = Piece<T>::pack(q);
+    }
+}
 
-// Blocks an SM and rounds of a block's threads over its items, for 8192 tokens of
-// 32 heads of 192 channels: six blocks and eight rounds 36.8 us; four rounds 42.6;
-// two or four items of a thread in flight in fewer blocks 37.2 to 46.7.
+// `rows` rows of d channels without the `gap` channels from `offset` on, copied;
+// COPIES pieces of a thread are in flight at a time.
+constexpr int COPIES = 4;
+
+template <typename T>
+__device__ __forceinline__ void copy_rows(const T *x, long long xs, T *y, long long ys, int rows, int d, int offset,
+                                          int gap, int self, int size)
+{
+    constexpr int P = Piece<T>::N;
+    if (d == gap) return;
+    Step e(self, size, (d - gap) / P);
+    while (e.row < rows) {
+        uint4 v[COPIES];
+        T *to[COPIES];
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k) {
+            to[k] = nullptr;
+            if (e.row < rows) {
+                const int c = e.at * P, at = c < offset ? c : c + gap;
+                v[k] = *reinterpret_cast<const uint4 *>(x + e.row * xs + at);
+                to[k] = y + e.row * ys + at;
+                e.next();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k)
+            if (to[k]) *reinterpret_cast<uint4 *>(to[k]) = v[k];
+    }
+}
+
+// Blocks an SM (a limit on registers) and 16-byte pieces of a thread, for 8192 tokens
+// of 32 heads of 192 channels: 6 and 8 33.4 us (6.0 TB/s, 92% of the measured copy
+// rate); 5 or 4 blocks 34.9 and 37.0 us, 8 blocks 41.3; 16 pieces 35.5, 32 42.4, 4
+// pieces 40.4.
 constexpr int BLOCKS = 6, ROUNDS = 8;
 
 template <typename T>
@@ -120,41 +150,29 @@ rope_kernel(const T *x, const int32_t *__restrict__ positions, const float *__re
             long long tokens, int H, int d, int rot, int offset, long long xs, long long os, int tpb,
             int heads, bool interleaved, bool inverse, float scale)
 {
-    // tpb tokens, and `heads` of their heads (blockIdx.y-th share)
-    extern __shared__ float2 cs[];                       // [tpb][rot / 2]
-    constexpr int P = Piece<T>::N;
+    // tpb tokens, each by NT / tpb threads, and `heads` of their heads (the blockIdx.y-th share)
+    extern __shared__ __align__(16) float2 cs[];         // [tpb][rot / 2]
     const long long t0 = (long long)blockIdx.x * tpb;
     const int nt = (int)min((long long)tpb, tokens - t0);
     const int h0 = blockIdx.y * heads, nh = min(heads, H - h0);
     const int half = rot / 2;
     for (int e = threadIdx.x; e < nt * half; e += NT)
         cs[e] = turn(positions[t0 + e / half], freqs[e % half], scale, inverse);
+    const int size = NT / tpb, t = threadIdx.x / size, self = threadIdx.x - t * size;
+    const T *xr = x + (t0 + t) * xs + (long long)h0 * d;
+    T *yr = out + (t0 + t) * os + (long long)h0 * d;
+    if (x != out && t < nt) copy_rows<T>(xr, d, yr, d, nh, d, offset, rot, self, size);
     __syncthreads();
-    // items of a head: the rotated ones, then (out of place) the other pieces two by two
-    const int nrot = rot / (2 * P), rest = (d - rot) / P;
-    const int per = nrot + (x == out ? 0 : (rest + 1) / 2);
-    const int all = nt * nh * per;
-    const float inv_per = 1.f / per, inv_nh = 1.f / nh;
-    for (int e = threadIdx.x; e < all; e += NT) {
-        const int th = quotient(e, inv_per), j = e - th * per;
-        const int t = quotient(th, inv_nh), h = h0 + th - t * nh;
-        const T *xr = x + (t0 + t) * xs + (long long)h * d;
-        T *yr = out + (t0 + t) * os + (long long)h * d;
-        Item<T> it;
-        if (j < nrot) {
-            it.turned(xr + offset, yr + offset, cs + t * half, j, rot, interleaved);
-        } else {
-            const int c = 2 * (j - nrot) * P, c2 = c + P;
-            it.copied(xr, yr, c < offset ? c : c + rot, c2 >= rest * P ? -1 : c2 < offset ? c2 : c2 + rot);
-        }
-        it.run(interleaved);
-    }
+    if (t < nt) turn_rows<T>(xr + offset, d, yr + offset, d, nh, rot, cs + t * half, interleaved, self, size);
 }
 
-constexpr int TPB = 8;          // tokens of an append block at most: one a warp
+// Tokens of an append block at most: 7167 tokens with 32 heads take 23.0 us with 4,
+// 23.9 with 8, 27.7 with 2 and 40.0 with 1 (a block first looks up where its tokens
+// go, four loads one after the other).
+constexpr int TPB = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(NT, 8)
+__global__ void __launch_bounds__(NT, BLOCKS)
 latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int32_t *__restrict__ table,
                      const int32_t *__restrict__ kv_lens, const int32_t *__restrict__ cu,
                      const T *__restrict__ q_pe, T *__restrict__ q, const float *__restrict__ freqs,
@@ -162,20 +180,19 @@ latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int3
                      int max_pages, long long page_stride, long long kvs, long long qts, long long qhs,
                      int tpb, bool interleaved, float scale, int *err)
 {
-    extern __shared__ float2 cs[];                       // [tpb][rot / 2]
+    // tpb tokens, each by 8 / tpb warps
+    extern __shared__ __align__(16) float2 cs[];         // [tpb][rot / 2]
     __shared__ long long place[TPB];                     // offset of the token's cache row, -1: skip
     __shared__ int where[TPB];                           // its position
-    constexpr int P = Piece<T>::N;
-    const int t0 = blockIdx.x * tpb, nt = min(tpb, tokens - t0);
-    const int warp = threadIdx.x >> 5;
-    if (warp < nt) {
-        const int t = t0 + warp;
-        const int n = paged::sequence_of(cu, N, per_seq, tokens, t);
-        if ((threadIdx.x & 31) == 0) {
+    const int size = NT / tpb, mine = threadIdx.x / size, self = threadIdx.x - mine * size;
+    const int t = blockIdx.x * tpb + mine;
+    if (self < 32) {
+        const int n = t < tokens ? paged::sequence_of(cu, N, per_seq, tokens, t) : N;
+        if (self == 0) {
             long long row = -1;
             int pos = 0;
             const int b = n < N ? paged::token_offset(cu, n, per_seq, tokens) : tokens;
-            if (t >= b) {                                // (else it belongs to no sequence: padding)
+            if (t < tokens && t >= b) {                  // (else it belongs to no sequence: padding)
                 const int e = paged::token_offset(cu, n + 1, per_seq, tokens);
                 const long long at = (long long)kv_lens[n] - (e - b) + (t - b);
                 int page = -1;
@@ -186,41 +203,27 @@ latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int3
                 if (page >= 0 && page < num_pages) row = page * page_stride + (long long)(pos % page_size) * dk;
                 else set_device_error(err, paged::kErrBadPage);
             }
-            place[warp] = row;
-            where[warp] = pos;
+            place[mine] = row;
+            where[mine] = pos;
         }
     }
     __syncthreads();
     const int half = rot / 2;
-    if (freqs) {
-        for (int e = threadIdx.x; e < nt * half; e += NT) cs[e] = turn(where[e / half], freqs[e % half], scale, false);
-        __syncthreads();
-    }
-    // items of a token: its latent (turned at the end, the rest copied), then each head of q
+    if (freqs)
+        for (int i = self; i < half; i += size) cs[mine * half + i] = turn(where[mine], freqs[i], scale, false);
+    const long long row = place[mine];
+    const T *src = kv + t * kvs;
     const int turned = freqs ? rot : 0;
-    const int nrot = turned / (2 * P), rest = (dk - turned) / P, nkv = nrot + (rest + 1) / 2;
-    const int nq = q ? rot / (2 * P) : 0;
-    const int per = nkv + nq * H;
-    const int all = nt * per;
-    const float inv_per = 1.f / per, inv_nq = nq ? 1.f / nq : 0.f;
-    for (int e = threadIdx.x; e < all; e += NT) {
-        const int t = tpb == 1 ? 0 : quotient(e, inv_per), j = e - t * per;
-        if (place[t] < 0) continue;
-        const float2 *c = cs + t * half;
-        Item<T> it;
-        if (j < nkv) {
-            const T *src = kv + (t0 + t) * kvs;
-            T *row = cache + place[t];
-            if (j < nrot) it.turned(src + dk - rot, row + dk - rot, c, j, rot, interleaved);
-            else it.copied(src, row, 2 * (j - nrot) * P, 2 * (j - nrot) + 1 < rest ? (2 * (j - nrot) + 1) * P : -1);
-        } else {
-            const int h = quotient(j - nkv, inv_nq), i = j - nkv - h * nq;
-            const T *src = q_pe + (t0 + t) * qts + h * qhs;
-            T *row = q + ((long long)(t0 + t) * H + h) * dk + dk - rot;
-            if (freqs) it.turned(src, row, c, i, rot, interleaved);
-            else it.copied(src, row, 2 * i * P, (2 * i + 1) * P);
-        }
-        it.run(interleaved);
+    if (row >= 0) copy_rows<T>(src, 0, cache + row, 0, 1, dk - turned, dk, 0, self, size);
+    __syncthreads();
+    if (row < 0) return;
+    const float2 *c = cs + mine * half;
+    if (freqs) turn_rows<T>(src + dk - rot, 0, cache + row + dk - rot, 0, 1, rot, c, interleaved, self, size);
+    if (q) {
+        const T *x = q_pe + t * qts;
+        T *y = q + (long long)t * H * dk + dk - rot;
+        if (freqs) turn_rows<T>(x, qhs, y, dk, H, rot, c, interleaved, self, size);
+        else copy_rows<T>(x, qhs, y, dk, H, rot, rot, 0, self, size);
     }
 }
 
@@ -229,19 +232,15 @@ cudaError_t rope_t(const void *x, const int32_t *positions, const float *freqs, 
                    int H, int d, int rot, int offset, long long xs, long long os, bool interleaved,
                    bool inverse, float scale, cudaStream_t st)
 {
-    // a block: ROUNDS items a thread, from several tokens or from a share of one token's heads
-    constexpr int P = Piece<T>::N;
-    const int per = x == out ? rot / (2 * P) : (d / P + 1) / 2;
-    const int want = ROUNDS * NT;
-    int heads = want / per;
+    // a block: about ROUNDS 16-byte pieces a thread, of up to eight tokens or of a share of one token's heads
+    const int per = (x == out ? rot : d) / Piece<T>::N;
+    int heads = ROUNDS * NT / per;
     heads = heads < 1 ? 1 : heads > H ? H : heads;
     int shares = (H + heads - 1) / heads;
     heads = (H + shares - 1) / shares;
     shares = (H + heads - 1) / heads;
-    int tpb = want / (heads * per);
-    tpb = shares > 1 || tpb < 1 ? 1 : tpb > 16 ? 16 : tpb;
-    // few tokens: no more than a round a block
-    while (tpb > 1 && tokens / tpb < 512) tpb >>= 1;
+    int tpb = 1;
+    while (shares == 1 && tpb < 8 && 2LL * tpb * H * per <= ROUNDS * NT && tokens / (2 * tpb) >= 512) tpb *= 2;
     const long long blocks = (tokens + tpb - 1) / tpb;
     if (blocks > 0x7fffffffLL || shares > 65535) return cudaErrorInvalidValue;
     rope_kernel<T><<<dim3((unsigned)blocks, shares), NT, sizeof(float2) * tpb * (rot / 2), st>>>(
@@ -255,9 +254,8 @@ cudaError_t append_t(const void *kv, void *cache, const PagedPlan &p, const void
                      int dk, int rot, long long kvs, long long qts, long long qhs, bool interleaved, float scale,
                      int *err, cudaStream_t st)
 {
-    // tokens of a block: up to eight (a warp each for their places), while 512 blocks and more are left;
-    // heads so many that quotient() would not be exact get one
-    int tpb = (long long)p.H * dk > (1 << 18) ? 1 : TPB;
+    // fewer tokens a block while there are not 512 blocks
+    int tpb = TPB;
     while (tpb > 1 && p.T / tpb < 512) tpb >>= 1;
     latent_append_kernel<T><<<(p.T + tpb - 1) / tpb, NT, sizeof(float2) * tpb * (rot / 2), st>>>(
         (const T *)kv, (T *)cache, p.page_table, p.kv_lens, p.cu_seqlens, (const T *)q_pe, (T *)q, freqs, p.T, p.H, dk,

@@ -571,8 +571,8 @@ kda_status kda_rope(const void *x, const int32_t *positions, const float *freqs,
  *   token at a negative position or without a valid page is not written, nor is
  *   its part of q, and sets the error word (code 5).
  * Supported: KDA_BF16 or KDA_F32; rot a multiple of 16 in [16, 1024] (or 0
- *   without q_pe and freqs), dk and strides multiples of 8, H * dk <= 2^24; kv,
- *   q_pe, q, cache 16-byte aligned.
+ *   without q_pe and freqs), dk and strides multiples of 8; kv, q_pe, q, cache
+ *   16-byte aligned.
  */
 kda_status kda_latent_append(const void *kv, void *cache, const int32_t *page_table,
                              const int32_t *kv_lens, const int32_t *cu_seqlens,

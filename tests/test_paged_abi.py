@@ -75,7 +75,7 @@ def test_attn_no_tokens_is_a_no_op(lib):
     dict(dk=580), dict(kvs=568), dict(kvs=580), dict(ts=100), dict(hs=60), dict(hs=72 + 4), dict(ts=32), dict(hs=32),
     dict(flags=32), dict(flags=1), dict(scale=INF), dict(scale=NAN), dict(dtype=-1), dict(kv=FAKE + 2),
     dict(cache=FAKE + 8), dict(q_pe=FAKE + 4), dict(q=FAKE + 8), dict(freqs=FAKE + 2), dict(ps=8), dict(ps=4),
-    dict(H=60000)])
+    dict(H=65536)])
 def test_append_bad_arguments_rejected(lib, kw):
     assert append(lib, **kw) == 1
     assert b"kda_latent_append" in lib.kda_last_error_message()
