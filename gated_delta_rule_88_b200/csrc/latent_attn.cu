@@ -18,13 +18,34 @@
 // device from kv_lens and cu_seqlens, are cut into one equal range per SM.  A row
 // tile that ends inside one range is finished there; its pieces in several
 // ranges go as (O, m, l) in fp32 to a workspace and latent_combine_kernel joins
-// them in a fixed order, so results do not depend on timing.
+// them in a fixed order, so results do not depend on timing.  Where that costs no
+// more, row tiles stay whole.
 //
 // Roles: four softmax warps per 32 rows (a thread has one key of S^T and 16 rows),
 // a TMA warp, and one warp each to issue the two products, so that S^T of the
 // next tile runs while the softmax of this one does.  Every wait is bounded and
 // watches an abort flag; a wait that runs out sets the device error word and the
 // block drains and returns.
+//
+// What bounds it (B200, bf16, dv 512, dk 576).  A product of M x N x 16 costs the
+// tensor pipe (32 M + 32 N) / 128 cycles, the time to read its operands from shared
+// memory, and its issue 36; a tile of 64 keys is 73.7 KB.
+//   R = 32 (one token of up to 32 heads): HBM.  64 sequences up to 8192 keys x 32
+//     heads: 73 us against 47.6 at the measured copy rate; a block's steady state is
+//     3.3 to 3.4 thousand cycles a tile (5.7 TB/s over all SMs), before it 3 us until
+//     the first load and 2 us in which the first tiles arrive together, after it 2 us
+//     for the last row tile and 5 for the second kernel.  2.5 tiles are in flight; 16 KB
+//     more did not help, nor did prefetching into L2 (it takes the loads' place in the
+//     queue).
+//   R = 64: the round of a stage through the block.  Q takes 74 KB, two tiles the
+//     rest: the second product ends, its stages are loaded anew (2.6 thousand cycles,
+//     1.6 of them the TMA unit's 62 + 1.84 per 128 bytes for each box), S^T, softmax
+//     (1.0), again the second product: 3.5 thousand a tile, where the products alone
+//     take 1.9.  4 sequences of up to 500 tokens behind up to 8192 keys: 767 us in
+//     pages of 64 (676 TFLOP/s, 41% of the measured dense rate), 860 in pages of 16, whose
+//     boxes are a quarter as long.
+//   128-key tiles (one in flight) took 95 us and 1.19 ms; one warp for both products
+//     115 us and 1.45 ms.
 #include "kernels.h"
 #include "paged.cuh"
 #include "prep_common.cuh"
@@ -98,7 +119,6 @@ struct Small {
     static constexpr int ONE = 35, ALL = 38;
     long long scan[12];
     int scan_rt[12], scan_max[12];
-    long long start_u;           // first unit of the block's row tile, counted over all
     int start[6];                // sequence, its first token, new tokens, keys; row tile; unit in it
     uint32_t tmem;
     int abort_flag;
@@ -828,7 +848,7 @@ latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta, _
     for (int e = 0; e < 2; ++e) {
         const int4 mt = meta[2 * blockIdx.x + e];
         if (mt.w == 0) continue;
-        const int pieces = mt.w, k0 = blockIdx.x - mt.z;
+        const int pieces = min(mt.w, (int)gridDim.x - mt.z), k0 = blockIdx.x - mt.z;
         const bool few = pieces <= FEW;
         auto at = [&](int k, int r) { return (size_t)(k == 0 ? 2 * mt.z + 1 : 2 * (mt.z + k)) * R + r; };
         // rows k0, k0 + pieces, ...: shared out over the warps of all y, or every y has its channels of each
