@@ -41,8 +41,8 @@
 //     rest: the second product ends, its stages are loaded anew (2.6 thousand cycles,
 //     1.6 of them the TMA unit's 62 + 1.84 per 128 bytes for each box), S^T, softmax
 //     (1.0), again the second product: 3.5 thousand a tile, where the products alone
-//     take 1.9.  4 sequences of up to 500 tokens behind up to 8192 keys: 767 us in
-//     pages of 64 (676 TFLOP/s, 41% of the measured dense rate), 860 in pages of 16, whose
+//     take 1.9.  4 sequences of up to 500 tokens behind up to 8192 keys: 762 us in
+//     pages of 64 (680 TFLOP/s, 41% of the measured dense rate), 859 in pages of 16, whose
 //     boxes are a quarter as long.
 //   128-key tiles (one in flight) took 95 us and 1.19 ms; one warp for both products
 //     115 us and 1.45 ms.
@@ -66,9 +66,11 @@ constexpr float TH = 60.f;
 // 64 sequences x 1 token 77.7, 76.6, 73, 72 and 75.
 constexpr int OV = 4;
 // What splitting costs a block, in key tiles (pieces written and joined): at 64
-// sequences x 4 tokens of 512 keys (8 tiles) 40.1 us split and 30.8 whole, at one
-// sequence of 300 keys 13.5 split and 18.5 whole; 8 picks the better of both in 108 of
-// 114 shapes of 1 to 200 sequences and 128 to 4096 keys, 6 and 10 in fewer.
+// sequences x 4 tokens of 512 keys (8 tiles) 41.2 us split and 30.9 whole, at one
+// sequence of 300 keys 13.9 split and 19.3 whole.  Over 108 shapes (1 to 200 sequences
+// of 128 to 4096 keys; 32 heads, 128, and 32 with 4 tokens) 8 comes within 3% and
+// 0.2 us of the better of both in 105, 6 in 107, 10 in 99; 6 and 8 have the same
+// geometric mean, 10 lies 1.4% above.
 constexpr int SPLIT_COST = 8;
 // Up to this many key tiles a sequence nothing is split, and the second kernel is not
 // even launched: one sequence of 128 keys 10.8 us instead of 11.8 (of 300 keys 16.8
@@ -488,7 +490,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         __nanosleep(32);
                     }
                 }
-                // what was issued, for the drain: a stage's use counts once its lanes are through
                 if (!ok) break;
                 st += L::MT;
                 if (st >= L::NS) { st -= L::NS; ++st_use; }
@@ -773,15 +774,18 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (a.lse && qd == 0 && lane < rows && !bad)
                     a.lse[row0 + 32 * cg + lane] = sum > 0.f ? (m_run + log2f(sum)) * 0.693147180559945f : -INFINITY;
                 __syncwarp();
-                for (int m = 0; m < L::MT; ++m) {
-                    float o[32];
-                    tmem_ld32(lanes + L::O_COL + m * R, o);
-                    tmem_wait_ld();
-                    __nv_bfloat16 *dst = a.out + (row0 + 32 * cg) * DV + 128 * m + t;
+                // (the test inside, at each store, spills what the loop over key tiles needs: 4 chunks
+                // of up to 500 tokens in pages of 64 took 801 us instead of 762)
+                if (!bad)
+                    for (int m = 0; m < L::MT; ++m) {
+                        float o[32];
+                        tmem_ld32(lanes + L::O_COL + m * R, o);
+                        tmem_wait_ld();
+                        __nv_bfloat16 *dst = a.out + (row0 + 32 * cg) * DV + 128 * m + t;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c < rows && !bad) dst[(size_t)c * DV] = __float2bfloat16_rn(o[c] * mine[c]);
-                }
+                        for (int c = 0; c < 32; ++c)
+                            if (c < rows) dst[(size_t)c * DV] = __float2bfloat16_rn(o[c] * mine[c]);
+                    }
             } else {
                 // a piece: slot 0 if it continues the row tile, slot 1 if it begins it
                 const size_t at = (size_t)(2 * b + (w.j0 == 0 ? 1 : 0)) * R + 32 * cg;
