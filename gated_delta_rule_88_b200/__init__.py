@@ -1,7 +1,8 @@
 """Kimi Delta Attention (KDA) token mixer for NVIDIA B200 (sm_100a).
 
 Thin Python binding over the C ABI in ``include/kda.h`` (``libkda_b200.so``):
-argument marshalling only.  Tensors must be CUDA tensors; every step of the
+argument marshalling only, by ctypes, and in C++ (``_paged.so``) for the paged
+operators.  Tensors must be CUDA tensors; every step of the
 computation runs in the library's kernels.  There is no CPU path: if the
 shared library is missing or cannot be loaded, calls raise.
 
@@ -557,63 +558,26 @@ def kda_state_affine(M, B, S_in, out=None):
     return out
 
 
-_ATTN_FULL, _ROPE_INTERLEAVED, _ROPE_INVERSE = 8, 16, 32
-_DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
-
 # The calls below run once a layer in every decoding step, where a few
-# microseconds on the host count: plain integers for pointers, one check a
-# tensor, and the device is switched only when it is another one.
+# microseconds on the host count: their checks, the allocation of results and the
+# call of the C ABI are C++ (csrc/binding.cpp).
+_ext = None
 
 
-def _on(t, name, idx, dtype):
-    """A contiguous tensor of the type on CUDA device idx."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != idx or not t.is_contiguous():
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.get_device() != idx:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{idx}")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _call(fn, idx, *args):
-    """fn(*args, stream) with CUDA device idx current, on its current stream."""
-    if torch._C._cuda_getDevice() == idx:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
-    else:
-        with torch.cuda.device(idx):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
-    if rc:
-        _check(rc)
-
-
-def _paged_args(who, T, cache, page_table, kv_lens, cu_seqlens, idx, dt, dk):
-    """Checks the cache's arrays; pointers (cache, page_table, kv_lens, cu_seqlens)
-    and sizes (num_seqs, num_pages, page_size, max_pages, page_stride)."""
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[2] != dk:
-        raise ValueError(f"{who}: cache must be [num_pages, page_size, {dk}]")
-    if cache.get_device() != idx or cache.dtype is not dt:
-        raise TypeError(f"{who}: cache must be {dt} on cuda:{idx}")
-    pages, psize, _ = cache.shape
-    stride, row, one = cache.stride()
-    if one != 1 or row != dk:
-        raise ValueError(f"{who}: the rows of a page must be contiguous")
-    if pages <= 1:
-        stride = psize * dk                    # (a pool of one page may report any stride)
-    tp, lp = _on(page_table, "page_table", idx, torch.int32), _on(kv_lens, "kv_lens", idx, torch.int32)
-    N = kv_lens.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != N or kv_lens.dim() != 1:
-        raise ValueError(f"{who}: page_table must be [num_seqs, max_pages] and kv_lens [num_seqs]")
-    cp = None
-    if cu_seqlens is not None:
-        cp = _on(cu_seqlens, "cu_seqlens", idx, torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() != N + 1:
-            raise ValueError(f"{who}: cu_seqlens must be [{N + 1}]")
-    elif N == 0 or T % N:
-        raise ValueError(f"{who}: without cu_seqlens the tokens must divide evenly over the sequences")
-    return (cache.data_ptr(), tp, lp, cp), (N, pages, psize, page_table.shape[1], stride)
+def _load_ext():
+    """The C++ binding, calling the library that load_library gives."""
+    global _ext
+    lib = load_library()
+    try:
+        from . import _paged
+    except ImportError as e:
+        raise RuntimeError("the binding _paged.so is missing or does not load: build it with "
+                           "`python -m gated_delta_rule_88_b200.build`") from e
+    names = ("kda_latent_attn", "kda_latent_append", "kda_rope", "kda_pages_copy", "kda_pages_compact",
+             "kda_last_error_message")
+    _paged.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, KDAError)
+    _ext = _paged
+    return _ext
 
 
 def kda_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=None, out=None, lse=None,
@@ -626,30 +590,7 @@ def kda_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=Non
     sees the keys up to its own position, else all of its sequence's.
     Returns (out [T,H,dv], lse [T,H] fp32); where they are allocated here, rows
     behind the last sequence are unspecified."""
-    lib = _lib or load_library()
-    idx = q.get_device()
-    if idx < 0:
-        raise ValueError("kda_latent_attn needs CUDA tensors (no CPU path)")
-    if q.dim() != 3:
-        raise ValueError("q must be [T,H,dk]")
-    T, H, dk = q.shape
-    dt = q.dtype
-    qp = _on(q, "q", idx, dt)
-    (cp, tp, lp, up), sizes = _paged_args("kda_latent_attn", T, cache, page_table, kv_lens, cu_seqlens, idx, dt, dk)
-    if out is None:
-        out = q.new_empty((T, H, dv))
-    elif out.shape != (T, H, dv):
-        raise ValueError(f"out must be [{T},{H},{dv}]")
-    if lse is None:
-        lse = q.new_empty((T, H), dtype=torch.float32)
-    elif lse.shape != (T, H):
-        raise ValueError(f"lse must be [{T},{H}]")
-    op, sp = _on(out, "out", idx, dt), _on(lse, "lse", idx, torch.float32)
-    if T == 0:
-        return out, lse
-    _call(lib.kda_latent_attn, idx, qp, cp, tp, lp, up, op, sp, T, H, dk, dv, *sizes,
-          dk ** -0.5 if scale is None else scale, 0 if causal else _ATTN_FULL, _DTYPES.get(dt, -1))
-    return out, lse
+    return (_ext or _load_ext()).latent_attn(q, cache, page_table, kv_lens, dv, cu_seqlens, out, lse, scale, causal)
 
 
 def kda_latent_append(kv, cache, page_table, kv_lens, q_pe=None, q=None, freqs=None, cu_seqlens=None,
@@ -659,46 +600,7 @@ def kda_latent_append(kv, cache, page_table, kv_lens, q_pe=None, q=None, freqs=N
     turned by the token's position, and q_pe [T,H,rot] (tokens and heads may be
     strided) likewise into q[..., dk-rot:] of q [T,H,dk].  Other arguments as
     kda_latent_attn."""
-    lib = _lib or load_library()
-    idx = kv.get_device()
-    if idx < 0:
-        raise ValueError("kda_latent_append needs CUDA tensors (no CPU path)")
-    if kv.dim() != 2:
-        raise ValueError("kv must be [T,dk]")
-    T, dk = kv.shape
-    dt = kv.dtype
-    kvs, one = kv.stride()
-    if T and (one != 1 or (T > 1 and kvs < dk)):
-        raise ValueError("kv must have contiguous rows, one after the other")
-    (cp, tp, lp, up), sizes = _paged_args("kda_latent_append", T, cache, page_table, kv_lens, cu_seqlens, idx, dt, dk)
-    H, rot, ts, hs = 1, 0, 0, 0
-    fp = pp = qp = None
-    if freqs is not None:
-        fp = _on(freqs, "freqs", idx, torch.float32)
-        rot = 2 * freqs.numel()
-    if (q_pe is None) != (q is None):
-        raise ValueError("q_pe and q come together")
-    if q_pe is not None:
-        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.get_device() != idx or q_pe.dtype is not dt:
-            raise ValueError(f"q_pe must be [{T},H,rot] {dt} on cuda:{idx}")
-        _, H, width = q_pe.shape
-        if freqs is not None and width != rot:
-            raise ValueError(f"q_pe must have {rot} channels, twice as many as freqs")
-        rot = width
-        ts, hs, one = q_pe.stride()
-        if T and H and one != 1:
-            raise ValueError("the heads of q_pe must be contiguous")
-        if (ts == 0 and T > 1) or (hs == 0 and H > 1):
-            raise ValueError("q_pe must not be broadcast")
-        ts, hs = ts if T > 1 else 0, hs if H > 1 else 0
-        pp, qp = q_pe.data_ptr(), _on(q, "q", idx, dt)
-        if q.shape != (T, H, dk):
-            raise ValueError(f"q must be [{T},{H},{dk}]")
-    if T == 0:
-        return
-    N, pages, psize, mp, stride = sizes
-    _call(lib.kda_latent_append, idx, kv.data_ptr(), cp, tp, lp, up, pp, qp, fp, T, H, dk, rot, N, pages, psize, mp, stride,
-          kvs if T > 1 else 0, ts, hs, _ROPE_INTERLEAVED if interleaved else 0, scale, _DTYPES.get(dt, -1))
+    (_ext or _load_ext()).latent_append(kv, cache, page_table, kv_lens, q_pe, q, freqs, cu_seqlens, interleaved, scale)
 
 
 def kda_rope(x, positions, freqs, out=None, offset: int = 0, interleaved: bool = False, inverse: bool = False,
@@ -708,50 +610,7 @@ def kda_rope(x, positions, freqs, out=None, offset: int = 0, interleaved: bool =
     positions int32 [T]; freqs fp32: radians a position of each pair (i, i +
     len(freqs)), or (2i, 2i + 1) if interleaved.  inverse: the transposed map,
     i.e. the gradient.  out may be x (in place)."""
-    lib = _lib or load_library()
-    idx = x.get_device()
-    if idx < 0:
-        raise ValueError("kda_rope needs CUDA tensors (no CPU path)")
-    if x.dim() != 3:
-        raise ValueError("x must be [T,H,d]")
-    T, H, d = x.shape
-
-    def stride(t, name):
-        ts, hs, one = t.stride()
-        if t.numel() and (one != 1 or (H > 1 and hs != d)):
-            raise ValueError(f"the heads of {name} must be contiguous")
-        if T <= 1:
-            return H * d
-        if ts == 0:
-            raise ValueError(f"{name} must not be broadcast")
-        return ts
-
-    xs = stride(x, "x")
-    pp, fp = _on(positions, "positions", idx, torch.int32), _on(freqs, "freqs", idx, torch.float32)
-    if positions.shape != (T,) or freqs.dim() != 1:
-        raise ValueError(f"positions must be [{T}] and freqs [rot / 2]")
-    if out is None:
-        out = x.new_empty((T, H, d))
-    elif out.shape != (T, H, d) or out.get_device() != idx or out.dtype is not x.dtype:
-        raise ValueError(f"out must be [{T},{H},{d}] {x.dtype} on cuda:{idx}")
-    if T == 0:
-        return out
-    _call(lib.kda_rope, idx, x.data_ptr(), pp, fp, out.data_ptr(), T, H, d, 2 * freqs.numel(), offset, xs,
-          stride(out, "out"), (_ROPE_INTERLEAVED if interleaved else 0) | (_ROPE_INVERSE if inverse else 0), scale,
-          _DTYPES.get(x.dtype, -1))
-    return out
-
-
-def _pool_args(who, pool, planes):
-    """(device index, planes, num_pages, page_bytes) of a contiguous pool [pages, ...] or [planes, pages, ...]."""
-    idx = pool.get_device() if isinstance(pool, torch.Tensor) else -1
-    if idx < 0:
-        raise ValueError(f"{who} needs CUDA tensors (no CPU path)")
-    numel = pool.numel()
-    if pool.dim() < (3 if planes else 2) or numel == 0 or not pool.is_contiguous():
-        raise ValueError(f"{who}: the pool must be a contiguous, non-empty [{'planes, ' if planes else ''}pages, ...]")
-    n, p = (pool.shape[0], pool.shape[1]) if planes else (1, pool.shape[0])
-    return idx, n, p, numel // (n * p) * pool.element_size()
+    return (_ext or _load_ext()).rope(x, positions, freqs, out, offset, interleaved, inverse, scale)
 
 
 def kda_pages_copy(pool, src, dst, planes: bool = False) -> None:
@@ -760,12 +619,7 @@ def kda_pages_copy(pool, src, dst, planes: bool = False) -> None:
     zeros for src[i] = -1.  src, dst int32 [n], n <= 4096; sources and
     destinations may overlap in any way; the last move to a destination counts.
     Works on a latent cache and on the state pool of kda_recurrent_steps."""
-    lib = _lib or load_library()
-    idx, n, p, nbytes = _pool_args("kda_pages_copy", pool, planes)
-    sp, dp = _on(src, "src", idx, torch.int32), _on(dst, "dst", idx, torch.int32)
-    if src.dim() != 1 or src.shape != dst.shape:
-        raise ValueError("src and dst must be [n]")
-    _call(lib.kda_pages_copy, idx, pool.data_ptr(), sp, dp, src.numel(), n, p, nbytes)
+    (_ext or _load_ext()).pages_copy(pool, src, dst, planes)
 
 
 def kda_pages_compact(pool, pages, planes: bool = False, out=None):
@@ -774,15 +628,7 @@ def kda_pages_compact(pool, pages, planes: bool = False, out=None):
     table; negative entries are padding; a page may be listed several times).
     With n distinct live pages, those at n and beyond go to the free indexes
     below n, both in ascending order.  out may be ``pages``."""
-    lib = _lib or load_library()
-    idx, n, p, nbytes = _pool_args("kda_pages_compact", pool, planes)
-    pp = _on(pages, "pages", idx, torch.int32)
-    if out is None:
-        out = torch.empty_like(pages)
-    elif out.shape != pages.shape:
-        raise ValueError("out must have the shape of pages")
-    _call(lib.kda_pages_compact, idx, pool.data_ptr(), pp, _on(out, "out", idx, torch.int32), pages.numel(), n, p, nbytes)
-    return out
+    return (_ext or _load_ext()).pages_compact(pool, pages, planes, out)
 
 
 def kda_get_device_error(stream=None) -> int:

@@ -1,12 +1,13 @@
-"""Build the KDA C-ABI shared library for sm_100a.
+"""Build the KDA C-ABI shared library for sm_100a, and the binding of its paged operators.
 
     python -m gated_delta_rule_88_b200.build [--force]
 
 Compiles every ``csrc/*.cu`` with nvcc (``-gencode arch=compute_100a,
 code=sm_100a -O3 -lineinfo``) into ``_build/`` at the repository root and
 links ``libkda_b200.so`` next to this file (in-tree, so it travels with the
-repository to the GPU host).  Rebuilds only when a source or header is newer
-than the library.
+repository to the GPU host).  ``csrc/binding.cpp`` is compiled by the host's
+compiler against torch's headers into ``_paged.so`` beside it.  Each is rebuilt
+only when a source or header of its own is newer.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda_b200.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+EXT = os.path.join(PKG, "_paged.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -45,7 +49,34 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    deps = [BINDING, os.path.join(INCLUDE, "kda.h")]
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(map(os.path.getmtime, deps)):
+        return EXT
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    dirs = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = EXT + f".tmp{os.getpid()}"
+    # (nvcc's own host compiler, whatever CXX says: a compiler without the shared C++ runtime links a second copy
+    # of it into the module, whose streams then crash in a process that has torch's)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[x for d in dirs for x in ("-isystem", d)], BINDING, "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {BINDING}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    build_binding(force, verbose)
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -2,6 +2,7 @@
 arguments return synchronously, before any CUDA call, with the status the
 header documents."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -134,3 +135,10 @@ def test_bindings_refuse_cpu_tensors():
                  lambda: kda.kda_pages_compact(x, i)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_binding_shares_the_process_cxx_runtime():
+    # a statically linked second copy of it crashes when it formats a message
+    with open(os.path.join(os.path.dirname(kda.library_path), "_paged.so"), "rb") as f:
+        image = f.read()
+    assert b"\0libstdc++.so.6\0" in image

@@ -15,6 +15,7 @@ Tolerances, derived from the number of roundings (bf16 rounds by at most u =
   page moves exact.
 """
 import itertools
+import threading
 
 import pytest
 import torch
@@ -756,3 +757,142 @@ def test_a_serving_run_of_a_hybrid():
         own = torch.zeros(1, H, d, d, device=DEV)
         ref = torch.cat([delta(own, i32(0), [s]) for s in seeds])
         assert torch.equal(ref[1], s2[0 if k == 0 else 2]) and torch.equal(ref[2], s3[k])
+
+
+def _refused_calls():
+    """name -> (exception, call on a dict of good arguments): what the binding or the library turns away on the host."""
+    V, Ty, K = ValueError, TypeError, kda.KDAError
+    return {
+        "attn q of two dimensions": (V, lambda a: kda.kda_latent_attn(a["q"][0], a["cache"], a["table"], a["lens"])),
+        "attn q strided": (V, lambda a: kda.kda_latent_attn(a["q"][:, ::2], a["cache"], a["table"], a["lens"])),
+        "attn q fp16": (Ty, lambda a: kda.kda_latent_attn(a["q"].half(), a["cache"], a["table"], a["lens"])),
+        "attn all fp16": (K, lambda a: kda.kda_latent_attn(a["q"].half(), a["cache"].half(), a["table"], a["lens"])),
+        "attn all fp32": (K, lambda a: kda.kda_latent_attn(a["q"].float(), a["cache"].float(), a["table"], a["lens"])),
+        "attn cache on the host": (Ty, lambda a: kda.kda_latent_attn(a["q"], a["cache"].cpu(), a["table"], a["lens"])),
+        "attn cache of other rows": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"][..., :512], a["table"], a["lens"])),
+        "attn page rows apart": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"][:, ::2], a["table"], a["lens"])),
+        "attn table of 64 bits": (Ty, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"].long(), a["lens"])),
+        "attn table strided": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"][:, ::2], a["lens"])),
+        "attn table of other rows": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"][:1], a["lens"])),
+        "attn lens on the host": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"].cpu())),
+        "attn no lens": (Ty, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], None)),
+        "attn offsets of other length": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], cu_seqlens=a["lens"])),
+        "attn tokens that do not divide": (V, lambda a: kda.kda_latent_attn(a["q"][:1], a["cache"], a["table"], a["lens"])),
+        "attn out of other shape": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], out=a["q"])),
+        "attn out of other type": (Ty, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"],
+                                                                     out=a["q"][..., :512].float().contiguous())),
+        "attn lse bf16": (Ty, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"],
+                                                            lse=a["q"][..., 0].contiguous())),
+        "attn scale inf": (K, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], scale=float("inf"))),
+        "attn dv negative": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], dv=-1)),
+        "attn dv 0": (K, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], dv=0)),
+        "attn dv past 32 bits": (V, lambda a: kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], dv=1 << 33)),
+        "append rows apart": (V, lambda a: kda.kda_latent_append(a["wide"][:, ::2], a["cache"], a["table"], a["lens"])),
+        "append broadcast rows": (V, lambda a: kda.kda_latent_append(a["kv"][:1].expand(2, 576), a["cache"], a["table"], a["lens"])),
+        "append q_pe alone": (V, lambda a: kda.kda_latent_append(a["kv"], a["cache"], a["table"], a["lens"], q_pe=a["q_pe"], freqs=a["freqs"])),
+        "append q alone": (V, lambda a: kda.kda_latent_append(a["kv"], a["cache"], a["table"], a["lens"], q=a["q"], freqs=a["freqs"])),
+        "append q_pe of other width": (V, lambda a: kda.kda_latent_append(a["kv"], a["cache"], a["table"], a["lens"], q_pe=a["q_pe"][..., :62],
+                                                                          q=a["q"], freqs=a["freqs"])),
+        "append q_pe broadcast": (V, lambda a: kda.kda_latent_append(a["kv"], a["cache"], a["table"], a["lens"], q_pe=a["q_pe"][:, :1].expand(2, 4, 64),
+                                                                     q=a["q"], freqs=a["freqs"])),
+        "append q of other heads": (V, lambda a: kda.kda_latent_append(a["kv"], a["cache"], a["table"], a["lens"], q_pe=a["q_pe"][:, :3],
+                                                                       q=a["q"], freqs=a["freqs"])),
+        "append freqs bf16": (Ty, lambda a: kda.kda_latent_append(a["kv"], a["cache"], a["table"], a["lens"], freqs=a["freqs"].bfloat16())),
+        "rope heads apart": (V, lambda a: kda.kda_rope(a["q"][:, ::2], a["lens"], a["freqs"])),
+        "rope positions of 64 bits": (Ty, lambda a: kda.kda_rope(a["q"], a["lens"].long(), a["freqs"])),
+        "rope positions of other length": (V, lambda a: kda.kda_rope(a["q"], a["lens"][:1], a["freqs"])),
+        "rope beyond the head": (K, lambda a: kda.kda_rope(a["q"], a["lens"], a["freqs"], offset=576)),
+        "rope offset past 32 bits": (V, lambda a: kda.kda_rope(a["q"], a["lens"], a["freqs"], offset=1 << 32)),
+        "rope out of other type": (V, lambda a: kda.kda_rope(a["q"], a["lens"], a["freqs"], out=a["q"].float())),
+        "rope out broadcast": (V, lambda a: kda.kda_rope(a["q"], a["lens"], a["freqs"], out=a["q"][:1].expand(2, 4, 576))),
+        "rope fp16": (K, lambda a: kda.kda_rope(a["q"].half(), a["lens"], a["freqs"])),
+        "copy pool strided": (V, lambda a: kda.kda_pages_copy(a["cache"][:, ::2], a["lens"], a["lens"])),
+        "copy lists of two lengths": (V, lambda a: kda.kda_pages_copy(a["cache"], a["lens"], a["lens"][:1])),
+        "copy lists of 64 bits": (Ty, lambda a: kda.kda_pages_copy(a["cache"], a["lens"].long(), a["lens"].long())),
+        "copy planes of a flat pool": (V, lambda a: kda.kda_pages_copy(a["cache"][0], a["lens"], a["lens"], planes=True)),
+        "copy empty pool": (V, lambda a: kda.kda_pages_copy(a["cache"][:0], a["lens"], a["lens"])),
+        "compact out of other shape": (V, lambda a: kda.kda_pages_compact(a["cache"], a["table"], out=a["lens"])),
+        "compact pages on the host": (V, lambda a: kda.kda_pages_compact(a["cache"], a["table"].cpu())),
+    }
+
+
+def _good_arguments():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    return dict(q=torch.ones(2, 4, 576, **bf), cache=torch.ones(6, 32, 576, **bf), kv=torch.ones(2, 576, **bf),
+                wide=torch.ones(2, 1152, **bf), q_pe=torch.ones(2, 4, 64, **bf), freqs=torch.ones(32, device="cuda"),
+                table=torch.arange(6, **i32).view(2, 3), lens=torch.tensor([3, 4], **i32))
+
+
+@pytest.mark.parametrize("what", list(_refused_calls()))
+def test_refused_calls_leave_everything_as_it_was(what):
+    error, call = _refused_calls()[what]
+    a = _good_arguments()
+    before = {k: v.clone() for k, v in a.items()}
+    with pytest.raises(error) as got:
+        call(a)
+    if error is kda.KDAError:
+        assert got.value.status in (1, 2) and "kda_" in str(got.value)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[k], before[k]) for k in a)
+    assert kda.kda_get_device_error() == 0
+    out, _ = kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"])      # the next call is not affected
+    assert torch.equal(out, torch.ones_like(out))
+
+
+def test_default_scale_and_accepted_forms():
+    a = _good_arguments()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    a["q"].normal_(generator=gen)
+    a["cache"].normal_(generator=gen)
+    want = kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], scale=576 ** -0.5)
+    got = kda.kda_latent_attn(q=a["q"], cache=a["cache"], page_table=a["table"], kv_lens=a["lens"], causal=1)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    whole = kda.kda_latent_attn(a["q"], a["cache"], a["table"], a["lens"], scale=1)
+    assert torch.isfinite(whole[0]).all()
+    none = kda.kda_latent_attn(a["q"][:0], a["cache"], a["table"], a["lens"])
+    assert none[0].shape == (0, 4, 512) and none[1].shape == (0, 4)
+    out = torch.empty_like(a["q"])
+    assert kda.kda_rope(a["q"], a["lens"], a["freqs"], out=out) is not None
+    assert torch.equal(out, kda.kda_rope(a["q"], a["lens"], a["freqs"]))
+
+
+def test_two_threads_call_at_once():
+    args = []
+    for seed in range(2):
+        a = _good_arguments()
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        a["q"].normal_(generator=gen)
+        a["cache"].normal_(generator=gen)
+        args.append(a)
+
+    def one(a):
+        x = kda.kda_rope(a["q"], a["lens"], a["freqs"], offset=512)
+        return kda.kda_latent_attn(x, a["cache"], a["table"], a["lens"])
+
+    want = [one(a) for a in args]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    got = one(args[i])
+                    if not (torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])):
+                        bad.append(i)
+                    try:
+                        kda.kda_rope(args[i]["q"], args[i]["lens"], args[i]["freqs"], offset=576 + i)
+                        bad.append("accepted")
+                    except kda.KDAError as e:            # each thread has its own message
+                        if f"offset={576 + i}" not in str(e):
+                            bad.append(str(e))
+        except Exception as e:
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:3]
