@@ -97,7 +97,7 @@ struct Lay {
     static constexpr uint32_t X_OFF = NQ * QP;                // the positional piece of the keys, two buffers
     static constexpr uint32_t P_OFF = X_OFF + (PE ? 2 * HALF : 0);
     static constexpr uint32_t ST_OFF = P_OFF + KT * R * 2;
-    static constexpr uint32_t SMALL = 3072;                   // barriers and small tables
+    static constexpr uint32_t SMALL = 3 * 1024;               // barriers and small tables
     static constexpr int NS = (SMEM - (int)SMALL - (int)ST_OFF) / (int)STAGE;
     static constexpr uint32_t MISC = ST_OFF + NS * STAGE;
     // TMEM: two S^T tiles (lanes +0 and +16 of the same columns), then O^T
@@ -127,7 +127,7 @@ struct Small {
     float red[8][32];            // a warp's result per row of its group
     float mine[8][32];           // a warp's own copy of a value per row of its group
 };
-static_assert(sizeof(Small) <= 3072, "small tables");
+static_assert(sizeof(Small) <= 3 * 1024, "small tables");
 
 struct Args {
     const int32_t *table, *lens, *cu;

@@ -611,7 +611,7 @@ kda_status kda_pages_copy(void *pool, const int32_t *src, const int32_t *dst, in
  * are unspecified.  An entry >= num_pages is copied and sets the device error
  * word (code 3).
  * Supported: as kda_pages_copy for the pool; num_pages <= 524288; count >= 0.
- * Memory: 4 * num_pages + 256 bytes from the library's pool.
+ * Memory: about 4 * num_pages + 264 bytes from the library's pool.
  */
 kda_status kda_pages_compact(void *pool, const int32_t *pages, int32_t *new_pages, long long count,
                              int planes, int num_pages, long long page_bytes, void *stream);
