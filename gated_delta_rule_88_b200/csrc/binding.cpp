@@ -124,7 +124,9 @@ Plan plan(const std::string &who, int64_t T, const Tensor &cache, const Tensor &
     p.pages = to_int(cache.size(0), "num_pages");
     p.page_size = to_int(cache.size(1), "page_size");
     p.max_pages = to_int(table.size(1), "max_pages");
-    // (a pool of one page may report any stride)
+    // (a pool of one page may report any stride; a page repeated by expand() has stride 0, which is no stride to hand
+    // on: to the library 0 stands for pages one after the other, which here lie behind the tensor's end)
+    if (cache.size(0) > 1 && cache.stride(0) < cache.size(1) * dk) bad_value(who + ": the pages of the cache must not overlap");
     p.stride = cache.size(0) > 1 ? cache.stride(0) : cache.size(1) * dk;
     return p;
 }
