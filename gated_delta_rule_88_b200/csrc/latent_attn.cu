@@ -645,8 +645,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int least = __reduce_min_sync(0xffffffffu, lane < rows ? sees : 0x7fffffff);
             // the segment's pages (one of a split tile's pieces with a bad page spoils all of it)
             bool bad = false;
-            const int lps = 31 - __clz(a.page_size), stop = min(w.j1 * KT, end);
-            for (int p = (w.j0 * KT >> lps) + t; p << lps < stop; p += 128) {
+            // (counted in pages: the keys of the next pages may lie past 2^31)
+            const int lps = 31 - __clz(a.page_size), stop = (min(w.j1 * KT, end) + a.page_size - 1) >> lps;
+            for (int p = (w.j0 * KT >> lps) + t; p < stop; p += 128) {
                 const int pg = a.table[(long long)w.n * a.max_pages + p];
                 bad |= pg < 0 || pg >= a.num_pages;
             }

@@ -4,11 +4,13 @@ header allows, against plain 64-bit forms and exact integer arithmetic (B200).
 The bounds of the attention's errors are those of test_paged_latent.py; others
 stand beside their tests.
 """
+import math
+
 import pytest
 import torch
 
 import gated_delta_rule_88_b200 as kda
-from test_paged_latent import DEV
+from test_paged_latent import DEV, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +31,28 @@ def test_cache_of_one_page_repeated_is_refused(how):
     # one page of any stride is a pool of one page
     out, _ = kda.kda_latent_attn(x, cache[:1], torch.zeros_like(table), lens)
     assert kda.kda_get_device_error() == 0 and torch.equal(out, torch.ones_like(out))
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("page", [16, 128])
+def test_attn_longest_sequence(page):
+    """2^31 - 256 keys, all of them in one page that the whole table names: the
+    answer is that page's.  Sums of 2^31 / 148 equal shares, a tile of 64 after
+    the other, in fp32: a thread's sum takes n / (148 64) additions of half a unit in
+    the last place at most (2^-24), the accumulators four products each, truncated
+    (2^-23); both relative to the sum of the absolute terms."""
+    n, dk, H = 2 ** 31 - 256, 256, 2
+    keys = torch.randn(page, dk, generator=gen(page)).to(torch.bfloat16)
+    q = torch.randn(1, H, dk, generator=gen(1)).to(torch.bfloat16)
+    table = torch.ones(1, n // page, dtype=torch.int32, device=DEV)
+    cache = torch.stack([torch.full_like(keys, float("nan")), keys]).to(DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    out, lse = kda.kda_latent_attn(q.to(DEV), cache, table, lens, dv=dk, scale=0.05)
+    assert kda.kda_get_device_error() == 0
+    x = torch.einsum("hd,kd->hk", q[0].double(), keys.double()) * 0.05
+    p = torch.softmax(x, -1)
+    tiles = n / (148 * 64)
+    size = p @ keys.double().abs()
+    sums = tiles * 2.0 ** -24
+    assert float((lse[0].double().cpu() - torch.logsumexp(x, -1) - math.log(n // page)).abs().max()) < 1.1 * sums + 1e-4
+    assert float(((out[0].double().cpu() - p @ keys.double()).abs() / size).max()) < 4 * tiles * 2.0 ** -23 + sums + 2.0 ** -7
