@@ -22,6 +22,12 @@ namespace {
 
 constexpr int NT = 256;
 
+// The kernels' limits on shared memory are set to what the largest calls take, never to what
+// this one does: the limit belongs to the function, and a call on another thread may set it
+// between this one's setting and its launch.
+constexpr size_t COPY_SMEM = 4096 * 32 + 4096 * 8 + 8192 * 8;      // 4096 moves, 32 bytes each
+constexpr size_t PLAN_SMEM = 524288 / 32 * 8;                      // 524,288 pages
+
 // Shared memory of a CTA: the moves' data, (source, destination) of each move
 // that counts, and a hash table {destination, last move to it} of `slots` entries
 // (a power of two >= 2 count).  piece = 16 << lsh bytes.
@@ -202,7 +208,8 @@ cudaError_t launch_pages_copy(void *pool, const int32_t *src, const int32_t *dst
     const long long ranges = (page_bytes + (16 << lsh) - 1) >> (lsh + 4);
     if (ranges > 0x7fffffffLL) return cudaErrorInvalidValue;
     const size_t smem = ((size_t)count << (lsh + 4)) + 8 * (size_t)count + 8 * (size_t)slots;
-    cudaError_t e = cudaFuncSetAttribute(pages_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > COPY_SMEM) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(pages_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)COPY_SMEM);
     if (e != cudaSuccess) return e;
     pages_copy_kernel<<<dim3((unsigned)ranges, planes), NT, smem, st>>>((unsigned char *)pool, src, dst, count,
                                                                         num_pages, page_bytes, lsh, slots, err);
@@ -214,7 +221,8 @@ cudaError_t launch_pages_compact(void *pool, const int32_t *pages, int32_t *new_
                                  cudaStream_t st)
 {
     const size_t smem = 8 * (size_t)((num_pages + 31) / 32);
-    cudaError_t e = cudaFuncSetAttribute(compact_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > PLAN_SMEM) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(compact_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PLAN_SMEM);
     if (e != cudaSuccess) return e;
     compact_plan_kernel<<<1, PLAN_NT, smem, st>>>(pages, new_pages, count, num_pages, scratch, err);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

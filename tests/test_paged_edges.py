@@ -5,6 +5,7 @@ The bounds of the attention's errors are those of test_paged_latent.py; others
 stand beside their tests.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -56,3 +57,54 @@ def test_attn_longest_sequence(page):
     sums = tiles * 2.0 ** -24
     assert float((lse[0].double().cpu() - torch.logsumexp(x, -1) - math.log(n // page)).abs().max()) < 1.1 * sums + 1e-4
     assert float(((out[0].double().cpu() - p @ keys.double()).abs() / size).max()) < 4 * tiles * 2.0 ** -23 + sums + 2.0 ** -7
+
+
+# ------------------------------------------------------------------ lists of any length from two threads
+def both_at_once(works):
+    """Runs the functions in threads, 300 times each; the first exceptions or answers other than None."""
+    bad, start = [], threading.Barrier(len(works))
+
+    def loop(work):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for _ in range(300):
+                    got = work()
+                    if got is not None:
+                        bad.append(got)
+        except Exception as e:
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=loop, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad[:3]
+
+
+def test_two_threads_copy_long_and_short_lists():
+    """The shared memory of a call (224 KB, a few KB) is no other call's limit."""
+    works, pools = [], []
+    for count in (4096, 3):
+        pool = torch.randn(5000, 4, generator=gen(count)).to(DEV)
+        src = torch.randperm(5000, generator=gen(count + 1))[:count].int().to(DEV)
+        pools.append((pool, pool.clone()))
+        works.append(lambda pool=pool, src=src: kda.kda_pages_copy(pool, src, src))          # each page onto itself
+    assert not both_at_once(works)
+    assert kda.kda_get_device_error() == 0
+    assert all(torch.equal(a, b) for a, b in pools)
+
+
+def test_two_threads_compact_large_and_small_pools():
+    works, checks = [], []
+    for n in (524288, 8):
+        pool = torch.randn(n, 4, generator=gen(n)).to(DEV)
+        live = torch.arange(3, dtype=torch.int32, device=DEV)                                 # in front already: nothing moves
+        out = torch.empty_like(live)
+        checks.append((pool, pool.clone(), out, live))
+        works.append(lambda pool=pool, live=live, out=out: (kda.kda_pages_compact(pool, live, out=out), None)[1])
+    assert not both_at_once(works)
+    assert kda.kda_get_device_error() == 0
+    assert all(torch.equal(a, b) and torch.equal(o, l) for a, b, o, l in checks)
