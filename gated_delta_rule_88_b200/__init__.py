@@ -45,6 +45,7 @@ Entry points (same names as the C ABI):
     kda_get_device_error(stream=None) -> int
     kda_selftest_bounded_wait(limit=1000): one CTA's bounded wait that always
                      runs out (sets device error code 1; no fault)
+    kda_selftest_latent_attn(...): kda_latent_attn with waits that give up at once
 """
 from __future__ import annotations
 
@@ -60,7 +61,7 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_ex", "kda_chunk_fwd_host", "kda_chunk
            "kda_recurrent_bwd", "kda_chunk_bwd", "kda_chunk_fwd_save", "kda_chunk_saved_bytes",
            "kda_chunk_bwd_saved",
            "kda_latent_attn", "kda_latent_append", "kda_rope", "kda_pages_copy", "kda_pages_compact",
-           "kda_get_device_error", "kda_selftest_bounded_wait",
+           "kda_get_device_error", "kda_selftest_bounded_wait", "kda_selftest_latent_attn",
            "KDAError",
            "KDA_QK_L2NORM", "KDA_BETA_SIGMOID", "KDA_STEPS_CHUNK",
            "library_path", "load_library"]
@@ -127,6 +128,8 @@ def load_library():
         lib.kda_state_affine.restype = i
         f, u = ctypes.c_float, ctypes.c_uint
         lib.kda_latent_attn.argtypes = [vp] * 7 + [i] * 8 + [ll, f, u, i, vp]
+        lib.kda_selftest_latent_attn.argtypes = lib.kda_latent_attn.argtypes
+        lib.kda_selftest_latent_attn.restype = i
         lib.kda_latent_append.argtypes = [vp] * 8 + [i] * 8 + [ll] * 4 + [u, f, i, vp]
         lib.kda_rope.argtypes = [vp] * 4 + [ll] + [i] * 4 + [ll] * 2 + [u, f, i, vp]
         lib.kda_pages_copy.argtypes = [vp] * 3 + [i] * 3 + [ll, vp]
@@ -573,7 +576,7 @@ def _load_ext():
     except ImportError as e:
         raise RuntimeError("the binding _paged.so is missing or does not load: build it with "
                            "`python -m gated_delta_rule_88_b200.build`") from e
-    names = ("kda_latent_attn", "kda_latent_append", "kda_rope", "kda_pages_copy", "kda_pages_compact",
+    names = ("kda_latent_attn", "kda_selftest_latent_attn", "kda_latent_append", "kda_rope", "kda_pages_copy", "kda_pages_compact",
              "kda_last_error_message")
     _paged.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, KDAError)
     _ext = _paged
@@ -650,3 +653,11 @@ def kda_selftest_bounded_wait(limit: int = 1000, device=None) -> None:
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
         _check(lib.kda_selftest_bounded_wait(int(limit), _stream_handle(dev)))
+
+
+def kda_selftest_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=None, out=None, lse=None,
+                             scale: float | None = None, causal: bool = True):
+    """kda_latent_attn (dk 576, dv 512) with waits that give up at once: every
+    block that has work leaves by the failure path, out and lse are not written
+    and the device error word reads 1."""
+    return (_ext or _load_ext()).selftest_latent_attn(q, cache, page_table, kv_lens, dv, cu_seqlens, out, lse, scale, causal)

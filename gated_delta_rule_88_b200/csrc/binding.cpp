@@ -26,6 +26,7 @@ using OptTensor = std::optional<Tensor>;
 namespace {
 
 decltype(&kda_latent_attn) f_attn;
+decltype(&kda_latent_attn) f_attn_selftest;
 decltype(&kda_latent_append) f_append;
 decltype(&kda_rope) f_rope;
 decltype(&kda_pages_copy) f_copy;
@@ -39,6 +40,7 @@ PyObject *error_type;            // KDAError(status, message)
 void init(const py::dict &f, const py::object &error) {
     auto address = [&](const char *name) { return f[name].cast<uintptr_t>(); };
     f_attn = reinterpret_cast<decltype(f_attn)>(address("kda_latent_attn"));
+    f_attn_selftest = reinterpret_cast<decltype(f_attn_selftest)>(address("kda_selftest_latent_attn"));
     f_append = reinterpret_cast<decltype(f_append)>(address("kda_latent_append"));
     f_rope = reinterpret_cast<decltype(f_rope)>(address("kda_rope"));
     f_copy = reinterpret_cast<decltype(f_copy)>(address("kda_pages_copy"));
@@ -131,8 +133,9 @@ Plan plan(const std::string &who, int64_t T, const Tensor &cache, const Tensor &
     return p;
 }
 
-py::tuple latent_attn(const Tensor &q, const Tensor &cache, const Tensor &table, const Tensor &lens, int64_t dv,
-                      const OptTensor &cu, const OptTensor &out_, const OptTensor &lse_, std::optional<double> scale, bool causal) {
+// f: kda_latent_attn or its self-test
+py::tuple attn_by(decltype(f_attn) f, const Tensor &q, const Tensor &cache, const Tensor &table, const Tensor &lens, int64_t dv,
+                  const OptTensor &cu, const OptTensor &out_, const OptTensor &lse_, std::optional<double> scale, bool causal) {
     const auto dev = device_of(q, "kda_latent_attn");
     if (q.dim() != 3) bad_value("q must be [T,H,dk]");
     const int64_t T = q.size(0), H = q.size(1), dk = q.size(2);
@@ -151,10 +154,21 @@ py::tuple latent_attn(const Tensor &q, const Tensor &cache, const Tensor &table,
     void *op = on(out, "out", dev, type);
     float *lp = (float *)on(lse, "lse", dev, at::kFloat);
     if (T > 0)
-        call(f_attn, dev, qp, (const void *)cache.data_ptr(), p.table, p.lens, p.cu, op, lp, to_int(T, "T"), to_int(H, "H"),
+        call(f, dev, qp, (const void *)cache.data_ptr(), p.table, p.lens, p.cu, op, lp, to_int(T, "T"), to_int(H, "H"),
              to_int(dk, "dk"), vd, p.N, p.pages, p.page_size, p.max_pages, p.stride,
              (float)(scale ? *scale : 1.0 / std::sqrt((double)dk)), causal ? 0u : (unsigned)KDA_ATTN_FULL, code);
     return py::make_tuple(std::move(out), std::move(lse));
+}
+
+py::tuple latent_attn(const Tensor &q, const Tensor &cache, const Tensor &table, const Tensor &lens, int64_t dv,
+                      const OptTensor &cu, const OptTensor &out, const OptTensor &lse, std::optional<double> scale, bool causal) {
+    return attn_by(f_attn, q, cache, table, lens, dv, cu, out, lse, scale, causal);
+}
+
+py::tuple selftest_latent_attn(const Tensor &q, const Tensor &cache, const Tensor &table, const Tensor &lens, int64_t dv,
+                               const OptTensor &cu, const OptTensor &out, const OptTensor &lse,
+                               std::optional<double> scale, bool causal) {
+    return attn_by(f_attn_selftest, q, cache, table, lens, dv, cu, out, lse, scale, causal);
 }
 
 void latent_append(const Tensor &kv, const Tensor &cache, const Tensor &table, const Tensor &lens, const OptTensor &q_pe,
@@ -264,6 +278,7 @@ Tensor pages_compact(const Tensor &pool, const Tensor &pages, bool planes, const
 PYBIND11_MODULE(_paged, m) {
     m.def("init", &init);
     m.def("latent_attn", &latent_attn);
+    m.def("selftest_latent_attn", &selftest_latent_attn);
     m.def("latent_append", &latent_append);
     m.def("rope", &rope);
     m.def("pages_copy", &pages_copy);

@@ -140,9 +140,11 @@ struct PagedPlan {
 // Attention of the new tokens over the cache (latent_attn.cu): bf16, dv in
 // {256, 512}, dk - dv in {0, 64}.  ws: latent_attn_workspace() bytes, 16-byte
 // aligned, with nothing in it that has to be set before; null if that is 0.
+// give_up: waits without polls, for the self-test (dv 512, dk 576).
 size_t latent_attn_workspace(const PagedPlan &p, int dv, int sms);
 cudaError_t launch_latent_attn(const void *q, const void *cache, const PagedPlan &p, void *out, float *lse,
-                               int dk, int dv, float scale, bool full, void *ws, int sms, int *err, cudaStream_t st);
+                               int dk, int dv, float scale, bool full, bool give_up, void *ws, int sms, int *err,
+                               cudaStream_t st);
 
 // New tokens into their pages, rotary positions on the last `rot` channels
 // (freqs null: none), and q's rotary part from q_pe (rope.cu).

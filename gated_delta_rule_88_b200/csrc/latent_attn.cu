@@ -250,9 +250,15 @@ struct Walk {
     }
 };
 
+// Polls of a wait before it gives up: half a second or more, none in the self-test.
+// (A constant: as an argument of the kernel it cost 3 us of 76 at 64 sequences to
+// 8192 keys and 1.2 of 16.4 at one sequence of 300.)
+template <bool GIVE_UP> constexpr uint32_t LIMIT = GIVE_UP ? 0 : 1u << 24;
+
+template <uint32_t POLLS>
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     if (mbar_test_wait(bar, parity)) return true;
-    for (uint32_t i = 0; i < (1u << 24); ++i) {
+    for (uint32_t i = 0; i < POLLS; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (i > 64) __nanosleep(32);
@@ -265,9 +271,10 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile
 __device__ __forceinline__ bool polled(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, bar == nullptr || mbar_test_wait(bar, parity));
 }
+template <uint32_t POLLS>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     if (polled(bar, parity)) return true;
-    return __all_sync(0xffffffffu, bar == nullptr || wait_on(bar, parity, abort_flag));
+    return __all_sync(0xffffffffu, bar == nullptr || wait_on<POLLS>(bar, parity, abort_flag));
 }
 
 // One lane of the warp, chosen by the hardware.  The products are issued by
@@ -333,11 +340,12 @@ __device__ __forceinline__ float across_lanes(float (&v)[16], int lane) {
     return v[0];
 }
 
-template <int R, int DV, bool PE>
+template <int R, int DV, bool PE, bool GIVE_UP>
 __global__ void __launch_bounds__(Lay<R, DV, PE>::NT, 1)
 latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c, const Args a)
 {
     using L = Lay<R, DV, PE>;
+    constexpr uint32_t POLLS = LIMIT<GIVE_UP>;
     extern __shared__ __align__(1024) unsigned char sm[];
     Small &z = *reinterpret_cast<Small *>(sm + L::MISC);
     volatile int *abort_flag = &z.abort_flag;
@@ -451,7 +459,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int end = w.s.keys_of(w.i);
             int boxes = boxes_of(w.j0, end);
             int page = page_of(w.j0, boxes, box), page_x = PE && lane < 4 ? page_of(w.j0, boxes, lane) : 0;
-            ok = segs == 0 || wait_on(&z.q_empty, (segs - 1) & 1, abort_flag);
+            ok = segs == 0 || wait_on<POLLS>(&z.q_empty, (segs - 1) & 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (lane == 0) {
                 const int row = w.s.first * a.H + w.i * R;
@@ -467,7 +475,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (PE) {
                     // (a positional piece is free long before the stages are)
                     uint64_t *eb = tiles < 2 ? nullptr : &z.x_empty[tiles & 1], *fb = &z.x_full[tiles & 1];
-                    if (!(ok = warp_wait(eb, ((tiles >> 1) - 1) & 1, abort_flag))) break;
+                    if (!(ok = warp_wait<POLLS>(eb, ((tiles >> 1) - 1) & 1, abort_flag))) break;
                     if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
                     if (lane < boxes && lane < 4)
                         prep::tma_load_3d(sm + L::X_OFF + (tiles & 1) * L::HALF + lane * rows_box * 128, &tm_c, DV,
@@ -485,7 +493,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         todo = false;
                     }
                     if ((tries & 63) == 0) {
-                        ok = tries < (1u << 24) && !*abort_flag;
+                        ok = tries < POLLS && !*abort_flag;
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
                         __nanosleep(32);
                     }
@@ -501,20 +509,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
         }
-        if (!ok) {
-            if (lane == 0) {
-                set_device_error(a.err, kErrWaitTimeout);
-                *abort_flag = 1;
-                // never leave with copies in flight into this block's shared memory; a tile that was
-                // begun when the wait ran out may have some of its boxes under way
-                for (int s = 0; s < L::NS; ++s)
-                    for (int k = 0; k < 2; ++k) mbar_wait(&z.full[s], k, 1u << 18);
-                for (int k = 0; k < 2; ++k) {
-                    for (int x = 0; PE && x < 2; ++x) mbar_wait(&z.x_full[x], k, 1u << 18);
-                    mbar_wait(&z.q_full, k, 1u << 18);
-                }
-            }
-        }
+        if (!ok && lane == 0) { set_device_error(a.err, kErrWaitTimeout); *abort_flag = 1; }
     } else if (warp == L::SW + 1) {
         // ---------------- S^T = C Q^T ----------------
         constexpr uint32_t ID = idesc(64, R, false);
@@ -548,7 +543,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 const bool all = polled(bar, parity);
                 // else one by one: S^T starts with what has landed
-                if (!all) ok = warp_wait(lane < L::MT ? nullptr : bar, parity, abort_flag);
+                if (!all) ok = warp_wait<POLLS>(lane < L::MT ? nullptr : bar, parity, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 if (PE) {
@@ -564,7 +559,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int m = 0; m < L::MT; ++m) {
                     const uint32_t k_lo = k_d.lo + (uniform_of(st) * L::STAGE >> 4), q_lo = q_d.lo + (2 * m * L::QP >> 4);
-                    if (ok && !all) ok = __all_sync(0xffffffffu, wait_on(&z.full[st], st_use & 1, abort_flag));
+                    if (ok && !all) ok = __all_sync(0xffffffffu, wait_on<POLLS>(&z.full[st], st_use & 1, abort_flag));
                     if (ok && elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
@@ -601,7 +596,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = true;
         for (; w.more() && ok; w.next(a))
             for (int j = w.j0; j < w.j1; ++j) {
-                if (!(ok = __all_sync(0xffffffffu, wait_on(&z.p_full, tiles & 1, abort_flag)))) break;
+                if (!(ok = __all_sync(0xffffffffu, wait_on<POLLS>(&z.p_full, tiles & 1, abort_flag)))) break;
                 tc_fence_after();
                 const uint32_t o = uniform_of(tmem) + L::O_COL, more = uniform_of((int)(j > w.j0));
 #pragma unroll
@@ -665,7 +660,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const bool dry = j < w.j0;
                 // S^T of this tile is there; O^T, P^T and the maxima of the previous one are done with
                 uint64_t *bar = dry ? nullptr : lane == 0 ? &z.s_full[tiles & 1] : lane == 1 && tiles > 0 ? &z.o_full : nullptr;
-                ok = ok && warp_wait(bar, lane == 0 ? (tiles >> 1) & 1 : (tiles - 1) & 1, abort_flag);
+                ok = ok && warp_wait<POLLS>(bar, lane == 0 ? (tiles >> 1) & 1 : (tiles - 1) & 1, abort_flag);
                 tc_fence_after();
                 float x[16], y[16];
                 tmem_ld_half(lanes + ((uint32_t)(16 * (tiles & 1)) << 16), x);
@@ -761,7 +756,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++tiles;
             }
             if (!ok) break;
-            ok = wait_on(&z.o_full, (tiles - 1) & 1, abort_flag);
+            ok = wait_on<POLLS>(&z.o_full, (tiles - 1) & 1, abort_flag);
             tc_fence_after();
             red[qd][lane] = across_lanes<false>(l, lane);
             if (named_bar_or(1 + cg, 128, !ok)) { ok = false; break; }
@@ -823,6 +818,18 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, L::COLS);
+    if (*abort_flag && warp == L::SW && lane == 0) {
+        // Some role gave up: never leave with copies in flight into this block's shared memory, whether the
+        // TMA warp gave up too or had issued its last tile before.  A barrier without copies, or of a tile
+        // that was not issued as a whole, takes all the polls (20 ms).
+        auto landed = [](uint64_t *bar) {
+            for (int k = 0; k < 2; ++k)
+                for (uint32_t i = 0; i < (1u << 18) && !mbar_test_wait(bar, k); ++i) __nanosleep(32);
+        };
+        for (int s = 0; s < L::NS; ++s) landed(&z.full[s]);
+        for (int x = 0; PE && x < 2; ++x) landed(&z.x_full[x]);
+        landed(&z.q_full);
+    }
 }
 
 // Joins the pieces of the row tiles that were split: with M = max m_k,
@@ -941,7 +948,7 @@ cudaError_t make_maps(CUtensorMap *q, CUtensorMap *c, const void *qp, const void
     return cudaSuccess;
 }
 
-template <int R, int DV, bool PE>
+template <int R, int DV, bool PE, bool GIVE_UP = false>
 cudaError_t launch_t(const void *q, const void *cache, const PagedPlan &p, void *out, float *lse, float scale, bool full,
                      void *ws, int sms, int *err, cudaStream_t st)
 {
@@ -964,9 +971,9 @@ cudaError_t launch_t(const void *q, const void *cache, const PagedPlan &p, void 
     a.split = ws != nullptr;
     a.err = err;
     const size_t smem = L::MISC + L::SMALL;
-    e = cudaFuncSetAttribute(latent_attn_kernel<R, DV, PE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(latent_attn_kernel<R, DV, PE, GIVE_UP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    latent_attn_kernel<R, DV, PE><<<sms, L::NT, smem, st>>>(mq, mc, a);
+    latent_attn_kernel<R, DV, PE, GIVE_UP><<<sms, L::NT, smem, st>>>(mq, mc, a);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.split) return e;
     return paged::launch_after(latent_combine_kernel<R, DV>, dim3(sms, CY), dim3(32 * CW), 0, st, a.ws_o, a.ws_ml, a.meta,
                                a.out, lse);
@@ -984,10 +991,15 @@ size_t latent_attn_workspace(const PagedPlan &p, int dv, int sms) {
 }
 
 cudaError_t launch_latent_attn(const void *q, const void *cache, const PagedPlan &p, void *out, float *lse,
-                               int dk, int dv, float scale, bool full, void *ws, int sms, int *err, cudaStream_t st)
+                               int dk, int dv, float scale, bool full, bool give_up, void *ws, int sms, int *err,
+                               cudaStream_t st)
 {
     const bool pe = dk != dv;
-#define KDA_LA(R, DV, PE) launch_t<R, DV, PE>(q, cache, p, out, lse, scale, full, ws, sms, err, st)
+#define KDA_LA(R, ...) launch_t<R, __VA_ARGS__>(q, cache, p, out, lse, scale, full, ws, sms, err, st)
+    if (give_up) {
+        if (dv != 512 || !pe) return cudaErrorNotSupported;
+        return rows_of_tile(p) == 32 ? KDA_LA(32, 512, true, true) : KDA_LA(64, 512, true, true);
+    }
     if (rows_of_tile(p) == 32)
         return dv == 512 ? (pe ? KDA_LA(32, 512, true) : KDA_LA(32, 512, false))
                          : (pe ? KDA_LA(32, 256, true) : KDA_LA(32, 256, false));

@@ -35,14 +35,12 @@ static kda_status check_plan(const char *fn, const kda::PagedPlan &p, int dk, kd
 
 static bool finite_f(float x) { return x == x && x <= 3.4028234e38f && x >= -3.4028234e38f; }
 
-extern "C" {
-
-kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page_table, const int32_t *kv_lens,
-                           const int32_t *cu_seqlens, void *out, float *lse, int T, int H, int dk, int dv,
-                           int num_seqs, int num_pages, int page_size, int max_pages, long long page_stride,
-                           float scale, unsigned flags, kda_dtype dtype, void *stream) {
+// kda_latent_attn; give_up: its waits do so at once.
+static kda_status latent_attn(const char *fn, bool give_up, const void *q, const void *cache, const int32_t *page_table,
+                              const int32_t *kv_lens, const int32_t *cu_seqlens, void *out, float *lse, int T, int H,
+                              int dk, int dv, int num_seqs, int num_pages, int page_size, int max_pages,
+                              long long page_stride, float scale, unsigned flags, kda_dtype dtype, void *stream) {
     kda::t_msg[0] = 0;
-    const char *fn = "kda_latent_attn";
     if (!q || !cache || !out) return fail(KDA_ERR_INVALID_ARG, "%s: null pointer argument", fn);
     if (page_stride == 0) page_stride = (long long)page_size * dk;
     const kda::PagedPlan p{page_table, kv_lens, cu_seqlens, T, H, num_seqs, num_pages, page_size, max_pages, page_stride};
@@ -66,12 +64,33 @@ kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page
     const size_t bytes = kda::latent_attn_workspace(p, dv, sms);
     if (bytes && (e = cudaMallocFromPoolAsync(&ws, bytes, mp, st)) != cudaSuccess)
         return cuda_fail(e, "kda_latent_attn workspace allocation");
-    e = kda::launch_latent_attn(q, cache, p, out, lse, dk, dv, scale, (flags & KDA_ATTN_FULL) != 0, ws, sms,
-                                kda::error_word(), st);
+    e = kda::launch_latent_attn(q, cache, p, out, lse, dk, dv, scale, (flags & KDA_ATTN_FULL) != 0, give_up,
+                                ws, sms, kda::error_word(), st);
     cudaError_t e2 = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
     if (e != cudaSuccess) return cuda_fail(e, "kda_latent_attn launch");
     if (e2 != cudaSuccess) return cuda_fail(e2, "kda_latent_attn workspace release");
     return KDA_OK;
+}
+
+extern "C" {
+
+kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page_table, const int32_t *kv_lens,
+                           const int32_t *cu_seqlens, void *out, float *lse, int T, int H, int dk, int dv,
+                           int num_seqs, int num_pages, int page_size, int max_pages, long long page_stride,
+                           float scale, unsigned flags, kda_dtype dtype, void *stream) {
+    return latent_attn("kda_latent_attn", false, q, cache, page_table, kv_lens, cu_seqlens, out, lse, T, H,
+                       dk, dv, num_seqs, num_pages, page_size, max_pages, page_stride, scale, flags, dtype, stream);
+}
+
+kda_status kda_selftest_latent_attn(const void *q, const void *cache, const int32_t *page_table, const int32_t *kv_lens,
+                                    const int32_t *cu_seqlens, void *out, float *lse, int T, int H, int dk, int dv,
+                                    int num_seqs, int num_pages, int page_size, int max_pages, long long page_stride,
+                                    float scale, unsigned flags, kda_dtype dtype, void *stream) {
+    kda::t_msg[0] = 0;
+    const char *fn = "kda_selftest_latent_attn";
+    if (dk != 576 || dv != 512) return fail(KDA_ERR_UNSUPPORTED, "%s: dk=%d dv=%d (supported: 576, 512)", fn, dk, dv);
+    return latent_attn(fn, true, q, cache, page_table, kv_lens, cu_seqlens, out, lse, T, H, dk, dv, num_seqs, num_pages,
+                       page_size, max_pages, page_stride, scale, flags, dtype, stream);
 }
 
 kda_status kda_latent_append(const void *kv, void *cache, const int32_t *page_table, const int32_t *kv_lens,

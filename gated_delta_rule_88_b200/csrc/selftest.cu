@@ -8,7 +8,8 @@
 // entry point launches one CTA whose thread 0 waits, with the caller's bound,
 // on an mbarrier that nothing ever arrives on -- no copy or MMA is in flight
 // -- so the host can check that such a timeout reaches kda_get_device_error()
-// and that the context stays usable afterwards.
+// and that the context stays usable afterwards.  (The way out with copies and MMAs
+// in flight: kda_selftest_latent_attn, paged_api.cu.)
 #include "../../include/kda.h"
 #include "api_internal.h"
 #include "sm100.cuh"

@@ -630,6 +630,20 @@ kda_status kda_pages_compact(void *pool, const int32_t *pages, int32_t *new_page
  */
 kda_status kda_selftest_bounded_wait(unsigned limit, void *stream);
 
+/*
+ * kda_selftest_latent_attn -- the same for the waits of kda_latent_attn, with
+ * copies and products in flight: that call with its own arguments (dk 576, dv
+ * 512), but each wait is asked once and then gives up.  The first wait of every
+ * block that has work runs out, as its data cannot be there yet: the blocks let
+ * their copies land, write nothing to out and lse, and the error word reads 1.
+ */
+kda_status kda_selftest_latent_attn(const void *q, const void *cache, const int32_t *page_table,
+                                    const int32_t *kv_lens, const int32_t *cu_seqlens, void *out,
+                                    float *lse, int T, int H, int dk, int dv, int num_seqs,
+                                    int num_pages, int page_size, int max_pages,
+                                    long long page_stride, float scale, unsigned flags,
+                                    kda_dtype dtype, void *stream);
+
 /* Static string for a status code. */
 const char *kda_status_string(kda_status s);
 

@@ -142,3 +142,11 @@ def test_binding_shares_the_process_cxx_runtime():
     with open(os.path.join(os.path.dirname(kda.library_path), "_paged.so"), "rb") as f:
         image = f.read()
     assert b"\0libstdc++.so.6\0" in image
+
+
+def test_latent_attn_selftest_refuses(lib):
+    args = [P(FAKE), P(FAKE), P(FAKE), P(FAKE), None, P(FAKE), None, 4, 2, 576, 512, 2, 8, 64, 4, 0, 1.0, 0, 1, None]
+    assert lib.kda_selftest_latent_attn(P(0), *args[1:]) == 1
+    assert b"kda_selftest_latent_attn" in lib.kda_last_error_message()
+    args[9] = 512
+    assert lib.kda_selftest_latent_attn(*args) == 2

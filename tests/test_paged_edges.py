@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import gated_delta_rule_88_b200 as kda
-from test_paged_latent import DEV, gen
+from test_paged_latent import DEV, Cache, check_attn, gen, oracle
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,25 @@ def test_two_threads_compact_large_and_small_pools():
     assert not both_at_once(works)
     assert kda.kda_get_device_error() == 0
     assert all(torch.equal(a, b) and torch.equal(o, l) for a, b, o, l in checks)
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("lens,count,H", [([40], 1, 32), ([40, 250], 1, 128), ([100, 130], 2, 32), ([6000, 9000], 1, 8),
+                                          ([6000], 4, 32)])
+def test_attn_waits_that_run_out(lens, count, H):
+    """The way out of a block with its copies under way (all of a short tile's, or
+    a long range's first ones): the error word is set, nothing is written, and
+    the next call is right."""
+    c = Cache(lens, 64, 576, seed=60)
+    cache, table, ln = c.to_gpu()
+    N, T = len(lens), len(lens) * count
+    q = torch.randn(T, H, 576, generator=gen(61)).to(torch.bfloat16)
+    qd = q.to(DEV)
+    out = torch.full((T, H, 512), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, H), 7.0, device=DEV)
+    kda.kda_selftest_latent_attn(qd, cache, table, ln, out=out, lse=lse, scale=0.07)
+    assert kda.kda_get_device_error() == 1
+    assert (out == 7).all() and (lse == 7).all()
+    kda.kda_latent_attn(qd, cache, table, ln, out=out, lse=lse, scale=0.07)
+    assert kda.kda_get_device_error() == 0
+    check_attn(out, lse, oracle(q, c.keys, [count] * N, 512, 0.07))
