@@ -58,9 +58,11 @@ using namespace sm100;
 
 constexpr int KT = 64;                        // keys of a tile
 // The reference m of a row's exponentials is the maximum of its first tile, and
-// is raised only when a later logit lies above it by this many powers of two: bf16
-// and fp32 keep their relative precision up to 2^127, so nothing is lost below that.
-constexpr float TH = 60.f;
+// is raised only when a later logit lies above it by more than TH powers of two: P up to
+// 2^TH keeps its relative precision in bf16, and O up to 2^TH kv_len max |c| in fp32 as long
+// as that is finite, hence the header's bound on kv_len times a value, 2^110.  (60 had
+// the same times, and overflowed from values of 2^67 on.)
+constexpr float TH = 16.f;
 // What a row tile costs besides its key tiles, in key tiles: 32 sequences x 4 tokens
 // up to 8000 keys take 101 us with 0, 93.7 with 1, 88 with 2, 84.6 with 4, 87.8 with 8;
 // 64 sequences x 1 token 77.7, 76.6, 73, 72 and 75.

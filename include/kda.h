@@ -511,7 +511,8 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * Layout: q [T, H, dk] dtype; out [T, H, dv] dtype; lse [T, H] float32 or NULL.
  * Cache rows at positions >= kv_len are never used and may hold anything;
  *   rows below it must be finite, as must q (of the tokens that count) and the
- *   logits x_j, above -1e30.
+ *   logits x_j, above -1e30; the largest magnitude of a value times kv_len must
+ *   stay below 2^110 (sums are formed in fp32, of probabilities up to 2^16).
  * Deterministic: the same call gives the same bits.
  * Memory: a stream-ordered workspace from the library's pool, of a size that
  *   depends on the device, H, T / num_seqs and dv only (at most 39 MB).

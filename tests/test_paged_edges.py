@@ -130,3 +130,27 @@ def test_attn_waits_that_run_out(lens, count, H):
     kda.kda_latent_attn(qd, cache, table, ln, out=out, lse=lse, scale=0.07)
     assert kda.kda_get_device_error() == 0
     check_attn(out, lse, oracle(q, c.keys, [count] * N, 512, 0.07))
+
+
+# ------------------------------------------------------------------ values and logits at the ends of their ranges
+@pytest.mark.parametrize("n", [250, 300])
+@pytest.mark.parametrize("rise", [15.5, 30.0, 59.0, 61.0, 200.0])
+def test_attn_large_values_above_a_low_first_tile(n, rise):
+    """Values of 2^100 whose logits rise by any amount after the first tile: the
+    answer is finite and stays so on the way (kv_len times a value < 2^110)."""
+    H, dk = 8, 576
+    c = Cache([n], 64, dk, seed=n)
+    k = torch.zeros(n, dk)
+    k[:, :512] = torch.randn(n, 512, generator=gen(1)).clamp(-1, 1) * 2.0 ** 100
+    k[64:, 512] = rise / 2                                   # powers of two above the first tile's logits
+    k[128:, 512] = rise
+    c.keys[0] = k.to(torch.bfloat16)
+    for j in range(c.table.shape[1]):
+        rows = c.keys[0][64 * j:64 * j + 64]
+        c.cache[c.table[0, j], :len(rows)] = rows
+    q = torch.zeros(1, H, dk, dtype=torch.bfloat16)
+    q[..., 512] = 1
+    cache, table, lens = c.to_gpu()
+    out, lse = kda.kda_latent_attn(q.to(DEV), cache, table, lens, scale=math.log(2))
+    assert kda.kda_get_device_error() == 0
+    check_attn(out, lse, oracle(q, c.keys, [1], 512, math.log(2)))
