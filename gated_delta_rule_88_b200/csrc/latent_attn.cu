@@ -768,9 +768,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const long long row0 = (long long)w.s.first * a.H + (long long)w.i * R;
             if (w.j0 == 0 && w.j1 == w.tiles) {
                 // the whole row tile was here
-                mine[lane] = sum > 0.f ? 1.f / sum : 0.f;
+                // (the sum of a row that sees a key is at least 1, or NaN, which is to show; 0: none)
+                mine[lane] = sum == 0.f ? 0.f : 1.f / sum;
                 if (a.lse && qd == 0 && lane < rows && !bad)
-                    a.lse[row0 + 32 * cg + lane] = sum > 0.f ? (m_run + log2f(sum)) * 0.693147180559945f : -INFINITY;
+                    a.lse[row0 + 32 * cg + lane] = sum == 0.f ? -INFINITY : (m_run + log2f(sum)) * 0.693147180559945f;
                 __syncwarp();
                 // (the test inside, at each store, spills what the loop over key tiles needs: 4 chunks
                 // of up to 500 tokens in pages of 64 took 801 us instead of 762)
@@ -898,7 +899,7 @@ latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta, _
                     for (int v = 0; v < V; ++v) add_scaled(acc[v], f, k == 0 ? first[0][v] : k == 1 ? first[1][v] : values(k)[32 * v]);
                     l = fmaf(f, x.y, l);
                 }
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     reinterpret_cast<uint2 *>(out + row * DV)[32 * v + lane] =
@@ -922,12 +923,12 @@ latent_combine_kernel(const float *ws_o, const float *ws_ml, const int4 *meta, _
                     add_scaled(acc, 1.f, part[k][lane]);
                     l += part_l[k];
                 }
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 reinterpret_cast<uint2 *>(out + row * DV)[32 * blockIdx.y + lane] =
                     make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
             }
             if (lane == 0 && lse && (few || blockIdx.y == 0))
-                lse[row] = l > 0.f ? (M + log2f(l)) * 0.693147180559945f : -INFINITY;
+                lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945f;
         }
     }
 }

@@ -512,7 +512,8 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * Cache rows at positions >= kv_len are never used and may hold anything;
  *   rows below it must be finite, as must q (of the tokens that count) and the
  *   logits x_j, above -1e30; the largest magnitude of a value times kv_len must
- *   stay below 2^110 (sums are formed in fp32, of probabilities up to 2^16).
+ *   stay below 2^110 (sums are formed in fp32, of probabilities up to 2^16).  A
+ *   NaN that a row sees all the same shows as NaN in its out and lse.
  * Deterministic: the same call gives the same bits.
  * Memory: a stream-ordered workspace from the library's pool, of a size that
  *   depends on the device, H, T / num_seqs and dv only (at most 39 MB).

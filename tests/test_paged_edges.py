@@ -154,3 +154,26 @@ def test_attn_large_values_above_a_low_first_tile(n, rise):
     out, lse = kda.kda_latent_attn(q.to(DEV), cache, table, lens, scale=math.log(2))
     assert kda.kda_get_device_error() == 0
     check_attn(out, lse, oracle(q, c.keys, [1], 512, math.log(2)))
+
+
+@pytest.mark.parametrize("n", [250, 300])
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_attn_nan_is_not_an_empty_row(where, n):
+    """A NaN in a query, or in a key that a row sees, shows in its out and lse; -inf
+    is the mark of a row that sees nothing."""
+    H = 32
+    c = Cache([n], 64, 576, seed=n)
+    q = torch.randn(1, H, 576, generator=gen(2)).to(torch.bfloat16)
+    if where == "query":
+        q[0, 5, 17] = float("nan")
+    cache, table, lens = c.to_gpu()
+    if where == "key":
+        cache[int(c.table[0, 1]), 6, 570] = float("nan")
+    out, lse = kda.kda_latent_attn(q.to(DEV), cache, table, lens, scale=0.07)
+    hit = torch.full((H,), where == "key")
+    hit[5] = True
+    assert lse[0, hit.to(DEV)].isnan().all() and out[0, hit.to(DEV)].isnan().all()
+    if where == "query":
+        q[0, 5] = 0
+        ref = oracle(q, c.keys, [1], 512, 0.07)
+        check_attn(out[:, ~hit.to(DEV)], lse[:, ~hit.to(DEV)], [x[:, ~hit] for x in ref])
