@@ -530,7 +530,7 @@ kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page
 /*
  * Rotary positions, shared by the two calls below.  Of `rot` consecutive
  * channels, pair i (0 <= i < rot / 2) is turned by the angle
- *     a = position * freqs[i]      (the product, reduced by whole turns, in fp64)
+ *     a = position * freqs[i]      (off by at most 2^-24 pi, at any position)
  *     (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a)
  * and rounded once.  Pair i is channels (i, i + rot / 2), or (2i, 2i + 1) with
  * KDA_ROPE_INTERLEAVED.  freqs: device float32 [rot / 2], so any base and any

@@ -6,6 +6,7 @@ stand beside their tests.
 """
 import math
 import threading
+from fractions import Fraction
 
 import pytest
 import torch
@@ -177,3 +178,44 @@ def test_attn_nan_is_not_an_empty_row(where, n):
         q[0, 5] = 0
         ref = oracle(q, c.keys, [1], 512, 0.07)
         check_attn(out[:, ~hit.to(DEV)], lse[:, ~hit.to(DEV)], [x[:, ~hit] for x in ref])
+
+
+# ------------------------------------------------------------------ angles
+def two_pi(bits):
+    """2 pi as an integer over 2^bits, by Machin's formula."""
+    one = 1 << (bits + 16)
+
+    def atan_inv(x):
+        term, total, k = one // x, 0, 0
+        while term:
+            total += term // (2 * k + 1) * (-1) ** k
+            term //= x * x
+            k += 1
+        return total
+
+    return (8 * (4 * atan_inv(5) - atan_inv(239))) >> 16
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_angle_at_any_position(interleaved):
+    """The angle is off by at most pi 2^-24 at any position and frequency: pairs
+    (1, 0) give the cosine and the sine, each off by that and one unit in the last
+    place of sincospif (2^-24 at most; the products with 1 and 0 are exact)."""
+    pos = [2142271631, 2 ** 31 - 1, -2 ** 31, 1, 0, -7, 1 << 20]
+    pos += torch.randint(-2 ** 31, 2 ** 31, (200,), generator=gen(3)).tolist()
+    freqs = torch.tensor([1.0, 0.7498942, 0.031622775, 1e-6, 37.5, 1000.3, 3.0e5, 6.2831855], dtype=torch.float32)
+    x = torch.zeros(len(pos), 1, 16)
+    x[..., slice(0, None, 2) if interleaved else slice(0, 8)] = 1
+    y = kda.kda_rope(x.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV), freqs.to(DEV), interleaved=interleaved)
+    y = y.double().cpu()[:, 0]
+    cos, sin = (y[:, 0::2], y[:, 1::2]) if interleaved else (y[:, :8], y[:, 8:])
+    bits = 260
+    turn = two_pi(bits)
+    tol = math.pi * 2.0 ** -24 + 2.0 ** -24
+    worst = 0.0
+    for t, p in enumerate(pos):
+        for i, f in enumerate(freqs.tolist()):
+            a = int(Fraction(f) * p * (1 << bits)) % turn
+            a = Fraction(a, 1 << bits)
+            worst = max(worst, abs(math.cos(a) - float(cos[t, i])), abs(math.sin(a) - float(sin[t, i])))
+    assert worst <= tol, f"{worst / tol:.2f} x the bound"
