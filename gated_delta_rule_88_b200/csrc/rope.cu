@@ -203,9 +203,11 @@ latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int3
             const int b = n < N ? paged::token_offset(cu, n, per_seq, tokens) : tokens;
             if (t < tokens && t >= b) {                  // (else it belongs to no sequence: padding)
                 const int e = paged::token_offset(cu, n + 1, per_seq, tokens);
-                const long long at = (long long)kv_lens[n] - (e - b) + (t - b);
+                const int len = kv_lens[n];
+                const long long at = (long long)len - (e - b) + (t - b);
                 int page = -1;
-                if (at >= 0 && at < (long long)max_pages * page_size) {
+                // (of a sequence of impossible length nothing is written; at < len whenever the offsets do not decrease)
+                if (at >= 0 && at < len && len <= (long long)max_pages * page_size) {
                     pos = (int)at;
                     page = table[(long long)n * max_pages + pos / page_size];
                 }

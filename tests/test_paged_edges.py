@@ -219,3 +219,27 @@ def test_rope_angle_at_any_position(interleaved):
             a = Fraction(a, 1 << bits)
             worst = max(worst, abs(math.cos(a) - float(cos[t, i])), abs(math.sin(a) - float(sin[t, i])))
     assert worst <= tol, f"{worst / tol:.2f} x the bound"
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("length", ["capacity + 1", "capacity + 5", "negative"])
+def test_append_writes_nothing_of_a_sequence_of_impossible_length(length):
+    c = Cache([20, 32, 40], 16, 576, seed=54)
+    cap = c.table.shape[1] * 16
+    for n in range(3):                                       # every entry is a page of its own
+        c.table[n] = torch.arange(3) + 3 * n
+    c.lens[1] = {"capacity + 1": cap + 1, "capacity + 5": cap + 5, "negative": -1}[length]
+    table, lens = c.table.to(DEV), c.lens.to(DEV)
+    cache = torch.full((9, 16, 576), 7.0, dtype=torch.bfloat16, device=DEV)
+    kv = torch.randn(15, 576, generator=gen(55)).to(torch.bfloat16).to(DEV)
+    q_pe = torch.randn(15, 2, 64, generator=gen(56)).to(torch.bfloat16).to(DEV)
+    q = torch.full((15, 2, 576), 7.0, dtype=torch.bfloat16, device=DEV)
+    kda.kda_latent_append(kv, cache, table, lens, q_pe=q_pe, q=q)
+    assert kda.kda_get_device_error() == 5
+    expect = torch.full_like(cache, 7.0)
+    for t in range(5):
+        expect[(15 + t) // 16, (15 + t) % 16] = kv[t]
+        expect[6 + (35 + t) // 16, (35 + t) % 16] = kv[10 + t]
+    assert torch.equal(cache, expect)
+    assert torch.equal(q[:5, :, 512:], q_pe[:5]) and torch.equal(q[10:, :, 512:], q_pe[10:])
+    assert (q[5:10] == 7).all() and (q[..., :512] == 7).all()
