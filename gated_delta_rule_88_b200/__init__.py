@@ -601,8 +601,8 @@ def kda_latent_append(kv, cache, page_table, kv_lens, q_pe=None, q=None, freqs=N
     """The new tokens' latents kv [T,dk] (tokens may be strided) into their
     pages of ``cache``; with freqs [rot/2] fp32 their last rot channels are
     turned by the token's position, and q_pe [T,H,rot] (tokens and heads may be
-    strided) likewise into q[..., dk-rot:] of q [T,H,dk].  Other arguments as
-    kda_latent_attn."""
+    strided) likewise into q[..., dk-rot:] of q [T,H,dk]; q_pe may be that slice
+    itself (in place).  Other arguments as kda_latent_attn."""
     (_ext or _load_ext()).latent_append(kv, cache, page_table, kv_lens, q_pe, q, freqs, cu_seqlens, interleaved, scale)
 
 

@@ -184,12 +184,13 @@ template <typename T>
 __global__ void __launch_bounds__(NT, BLOCKS)
 latent_append_kernel(const T *__restrict__ kv, T *__restrict__ cache, const int32_t *__restrict__ table,
                      const int32_t *__restrict__ kv_lens, const int32_t *__restrict__ cu,
-                     const T *__restrict__ q_pe, T *__restrict__ q, const float *__restrict__ freqs,
+                     const T *q_pe, T *q, const float *__restrict__ freqs,
                      int tokens, int H, int dk, int rot, int N, int per_seq, int num_pages, int page_size,
                      int max_pages, long long page_stride, long long kvs, long long qts, long long qhs,
                      int tpb, bool interleaved, float scale, int *err)
 {
-    // tpb tokens, each by 8 / tpb warps
+    // tpb tokens, each by 8 / tpb warps.  q_pe may be the channels of q that it is written to: each
+    // piece is read and written by one thread.
     extern __shared__ __align__(16) float2 cs[];         // [tpb][rot / 2]
     __shared__ long long place[TPB];                     // offset of the token's cache row, -1: skip
     __shared__ int where[TPB];                           // its position

@@ -566,6 +566,8 @@ kda_status kda_rope(const void *x, const int32_t *positions, const float *freqs,
  *   the token's position.  q_pe [T, H, rot] dtype, elements q_pe_ts between
  *   tokens (0: H * q_pe_hs) and q_pe_hs between heads (0: rot), turned alike and
  *   written to q[t, h, dk - rot : dk] of q [T, H, dk]; both NULL: no queries.
+ *   q_pe may be those very channels of q (in place: q + dk - rot, q_pe_ts = H * dk,
+ *   q_pe_hs = dk), else it must not overlap them; nor must kv overlap the cache.
  *   freqs NULL: nothing is turned (layers without positions); rot is then only
  *   the width of q_pe.  flags: KDA_ROPE_INTERLEAVED or 0.
  * Tokens of one call must go to distinct cache rows (pages shared by several

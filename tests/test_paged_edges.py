@@ -243,3 +243,25 @@ def test_append_writes_nothing_of_a_sequence_of_impossible_length(length):
     assert torch.equal(cache, expect)
     assert torch.equal(q[:5, :, 512:], q_pe[:5]) and torch.equal(q[10:, :, 512:], q_pe[10:])
     assert (q[5:10] == 7).all() and (q[..., :512] == 7).all()
+
+
+@pytest.mark.parametrize("T,H", [(3, 33), (2051, 4)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("positions", ["halves", "interleaved", "none"])
+def test_append_turns_the_queries_in_place(T, H, dtype, positions):
+    """q_pe is the slice of q that is written: the bits of a call with a copy of it."""
+    g = gen(T)
+    kv, q = torch.randn(T, 128, generator=g).to(DEV, dtype), torch.randn(T, H, 128, generator=g).to(DEV, dtype)
+    pages = -(-T // 16)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    freqs = None if positions == "none" else (10000.0 ** (-torch.arange(32) / 32.0)).to(DEV)
+    made = []
+    for copied in (True, False):
+        mine, cache = q.clone(), torch.zeros(pages, 16, 128, dtype=dtype, device=DEV)
+        part = mine[..., 64:].contiguous() if copied else mine[..., 64:]
+        kda.kda_latent_append(kv, cache, table, lens, q_pe=part, q=mine, freqs=freqs, interleaved=positions == "interleaved")
+        made.append((mine, cache))
+    assert kda.kda_get_device_error() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*made))
+    assert torch.equal(made[0][0], q) == (positions == "none")
