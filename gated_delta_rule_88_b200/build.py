@@ -6,8 +6,9 @@ Compiles every ``csrc/*.cu`` with nvcc (``-gencode arch=compute_100a,
 code=sm_100a -O3 -lineinfo``) into ``_build/`` at the repository root and
 links ``libkda_b200.so`` next to this file (in-tree, so it travels with the
 repository to the GPU host).  ``csrc/binding.cpp`` is compiled by the host's
-compiler against torch's headers into ``_paged.so`` beside it.  Each is rebuilt
-only when a source or header of its own is newer.
+compiler against torch's headers into ``_paged.so`` beside it, after the library,
+which needs nvcc alone.  Each is rebuilt only when a source or header of its own
+is newer; the binding also when it was built for another torch or Python.
 """
 from __future__ import annotations
 
@@ -49,9 +50,25 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _built_for() -> str:
+    """What a binding goes with, as it is written into the module."""
+    import torch
+
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def needs_binding() -> bool:
+    if not os.path.exists(EXT):
+        return True
+    t = os.path.getmtime(EXT)
+    if any(os.path.getmtime(p) > t for p in (BINDING, os.path.join(INCLUDE, "kda.h"))):
+        return True
+    with open(EXT, "rb") as f:
+        return f"\0{_built_for()}\0".encode() not in f.read()
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    deps = [BINDING, os.path.join(INCLUDE, "kda.h")]
-    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(map(os.path.getmtime, deps)):
+    if not force and not needs_binding():
         return EXT
     import torch
 
@@ -64,7 +81,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     # of it into the module, whose streams then crash in a process that has torch's)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           *[x for d in dirs for x in ("-isystem", d)], BINDING, "-o", tmp, "-L", os.path.join(home, "lib"),
+           f'-DKDA_BUILT_FOR="{_built_for()}"', *[x for d in dirs for x in ("-isystem", d)], BINDING, "-o", tmp, "-L", os.path.join(home, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -76,7 +93,12 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    build_library(force, verbose, extra)
     build_binding(force, verbose)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

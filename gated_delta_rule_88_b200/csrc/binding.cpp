@@ -275,7 +275,12 @@ Tensor pages_compact(const Tensor &pool, const Tensor &pages, bool planes, const
 
 }  // namespace
 
+// the torch and Python that this was compiled against (build.py looks for it in the module's bytes)
+extern const char built_for[];
+const char built_for[] = "\0" KDA_BUILT_FOR;
+
 PYBIND11_MODULE(_paged, m) {
+    m.attr("built_for") = built_for + 1;
     m.def("init", &init);
     m.def("latent_attn", &latent_attn);
     m.def("selftest_latent_attn", &selftest_latent_attn);
