@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import gated_delta_rule_88_b200 as kda
-from test_paged_latent import DEV, Cache, check_attn, gen, oracle
+from test_paged_latent import DEV, Cache, check_attn, check_rotated, freqs_of, gen, oracle, rotate64, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -265,3 +265,170 @@ def test_append_turns_the_queries_in_place(T, H, dtype, positions):
     assert kda.kda_get_device_error() == 0
     assert all(torch.equal(a, b) for a, b in zip(*made))
     assert torch.equal(made[0][0], q) == (positions == "none")
+
+
+# ------------------------------------------------------------------ many row tiles, many tokens
+def oracle_on_gpu(q, keys, counts, dv, scale):
+    """oracle() of test_paged_latent.py for long causal chunks: whole sequences at once, on the GPU in 64 bits."""
+    dk, H = q.shape[2], q.shape[1]
+    parts, t = [], 0
+    for k, count in zip(keys, counts):
+        if not count:
+            continue
+        k, x = k.to(DEV).double(), q[t:t + count].to(DEV).double().reshape(-1, q.shape[2])
+        see = len(k) - count + torch.arange(count, device=DEV).repeat_interleave(H) + 1
+        hidden = torch.arange(len(k), device=DEV)[None] >= see[:, None]
+        logits = (x @ k.T * scale).masked_fill_(hidden, -float("inf"))
+        size = abs(scale) * (x.abs() @ k.abs().T).masked_fill_(hidden, 0).amax(-1)
+        none = see <= 0
+        p = torch.softmax(logits, -1).masked_fill_(none[:, None], 0)
+        X = ((dk + 8) * 2.0 ** -24 * size + 2.0 ** -22)[:, None]
+        A = p @ k[:, :dv].abs()
+        o, l = p @ k[:, :dv], torch.logsumexp(logits, -1)
+        tol = 2.0 ** -8 * (o.abs() + A) * (1 + 2.0 ** -7) + 2 * X * A + 1e-30
+        ltol = X[:, 0] + 2.0 ** -22 * (1 + l.abs())
+        parts.append([z.view(count, H, -1).cpu() if z.dim() == 2 else z.view(count, H).cpu() for z in (o, l, tol, ltol)])
+        t += count
+    return [torch.cat(z) for z in zip(*parts)]
+
+
+@pytest.mark.parametrize("counts,lens,H,page,dv,dr,empty", [
+    ([700, 500, 650, 333], [1200, 500, 901, 2000], 32, 64, 512, 64, 0),
+    ([400, 391], [1500, 391], 20, 16, 512, 64, 0),
+    ([1300], [1300], 33, 128, 256, 0, 0),
+    ([300, 260], [1111, 255], 32, 32, 512, 64, 600),                   # 32-row tiles: most sequences are empty
+])
+def test_attn_many_row_tiles_of_a_sequence(counts, lens, H, page, dv, dr, empty):
+    """Long causal chunks: several row tiles of a sequence for each SM, of different numbers of key tiles."""
+    c = Cache(lens, page, dv + dr, seed=H)
+    if empty:
+        c.lens = torch.cat([c.lens, torch.zeros(empty, dtype=torch.int32)])
+        c.table = torch.cat([c.table, torch.full((empty, c.table.shape[1]), -1, dtype=torch.int32)])
+        counts = counts + [0] * empty
+    q, out, lse, scale = run_attn(c, counts, H, dv, varlen=True)
+    assert kda.kda_get_device_error() == 0
+    ref = oracle_on_gpu(q, c.keys, counts, dv, scale)
+    check_attn(out, lse, ref)
+
+
+@pytest.mark.parametrize("T,H,d,rot,offset,dtype", [(8195, 3, 64, 32, 16, torch.bfloat16), (2051, 2, 96, 96, 0, torch.float32),
+                                                    (7, 33, 576, 64, 512, torch.float32), (4100, 1, 16, 16, 0, torch.bfloat16)])
+def test_rope_blocks_of_several_tokens_and_shares_of_heads(T, H, d, rot, offset, dtype):
+    x = torch.randn(T, H, d, generator=gen(T)).to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=gen(T + 1), dtype=torch.int32)
+    f = freqs_of(rot)
+    y = kda.kda_rope(x.to(DEV), pos.to(DEV), f.to(DEV), offset=offset)
+    part = x[..., offset:offset + rot]
+    check_rotated(y[..., offset:offset + rot], part, rotate64(part, pos, f, False), False, 1.0)
+    keep = torch.ones(d, dtype=torch.bool)
+    keep[offset:offset + rot] = False
+    assert torch.equal(y.cpu()[..., keep], x[..., keep])
+
+
+@pytest.mark.parametrize("T,H", [(1026, 5), (2200, 3)])
+def test_append_blocks_of_several_tokens(T, H):
+    """Blocks of 2 and 4 tokens, with rows behind the last sequence in the last one."""
+    extra, page, dk, rot = 3, 32, 192, 64
+    counts = [T // 3, 0, T - T // 3]
+    lens = [counts[0] + 77, 5, counts[2]]
+    c = Cache(lens, page, dk, seed=T)
+    cache, table, ln = c.to_gpu()
+    before = cache.clone()
+    kv = torch.randn(T + extra, dk, generator=gen(1)).to(torch.bfloat16)
+    q_pe = torch.randn(T + extra, H, rot, generator=gen(2)).to(torch.bfloat16)
+    q = torch.full((T + extra, H, dk), 7.0, dtype=torch.bfloat16, device=DEV)
+    cu = torch.tensor([0, counts[0], counts[0], T], dtype=torch.int32, device=DEV)
+    f = freqs_of(rot)
+    kda.kda_latent_append(kv.to(DEV), cache, table, ln, q_pe=q_pe.to(DEV), q=q, freqs=f.to(DEV), cu_seqlens=cu)
+    assert kda.kda_get_device_error() == 0
+    seq = torch.tensor([0] * counts[0] + [2] * counts[2])
+    pos = torch.cat([torch.arange(counts[0]) + 77, torch.arange(counts[2])])
+    ids, rows = c.table[seq, pos // page].long(), pos % page
+    got = cache[ids.to(DEV), rows.to(DEV)].cpu()
+    assert torch.equal(got[:, :dk - rot], kv[:T, :dk - rot])
+    part = kv[:T, None, dk - rot:]
+    check_rotated(got[:, None, dk - rot:], part, rotate64(part, pos, f, False), False, 1.0)
+    check_rotated(q[:T, :, dk - rot:], q_pe[:T], rotate64(q_pe[:T], pos, f, False), False, 1.0)
+    assert (q[T:] == 7).all() and (q[..., :dk - rot] == 7).all()
+    before[ids.to(DEV), rows.to(DEV)] = got.to(DEV)                    # nothing else was written
+    assert torch.equal(torch.nan_to_num(cache.float(), 123.0), torch.nan_to_num(before.float(), 123.0))
+
+
+# ------------------------------------------------------------------ a step as a graph
+def test_a_captured_step_of_all_calls():
+    """Fork, append, attention, compaction and a rotation in one graph, replayed on
+    other inputs, beside the same calls made eagerly on copies."""
+    H, dk, page, N = 4, 576, 16, 3
+    i32 = dict(dtype=torch.int32, device=DEV)
+    f = freqs_of(64).to(DEV)
+
+    def inputs(seed):
+        g = gen(seed)
+        lens = torch.randint(17, 48, (N,), generator=g, dtype=torch.int32)
+        table = torch.full((N, 3), -1, dtype=torch.int32)
+        ids = torch.randperm(20, generator=g)[:9].int().view(N, 3)
+        for n in range(N):
+            table[n, :-(-int(lens[n]) // page)] = ids[n, :-(-int(lens[n]) // page)]
+        # the first sequence's last page is copied to a free one, and named by its table
+        last = (int(lens[0]) - 1) // page
+        free = [i for i in range(20) if i not in ids.flatten().tolist()][0]
+        src, dst = table[0, last:last + 1].clone(), torch.tensor([free], dtype=torch.int32)
+        table[0, last] = free
+        return [torch.randn(20, page, dk, generator=g).to(torch.bfloat16), table, lens, src, dst,
+                torch.randn(N, dk, generator=g).to(torch.bfloat16), torch.randn(N, H, dk, generator=g).to(torch.bfloat16)]
+
+    def step(cache, table, lens, src, dst, kv, q):
+        kda.kda_pages_copy(cache, src, dst)
+        kda.kda_latent_append(kv, cache, table, lens, q_pe=q[..., 512:], q=q, freqs=f)
+        a = kda.kda_latent_attn(q, cache, table, lens, scale=0.07)
+        kda.kda_pages_compact(cache, table, out=table)
+        b = kda.kda_latent_attn(q, cache, table, lens, scale=0.07)
+        return [*a, *b, kda.kda_rope(q, lens, f, offset=512, inverse=True)]
+
+    held = [x.to(DEV) for x in inputs(0)]
+    step(*[x.clone() for x in held])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        made = step(*held)
+    for seed in range(1, 9):
+        new = [x.to(DEV) for x in inputs(seed)]
+        for h, x in zip(held, new):
+            h.copy_(x)
+        graph.replay()
+        eager = step(*new)
+        torch.cuda.synchronize()
+        assert kda.kda_get_device_error() == 0
+        assert all(torch.equal(a, b) for a, b in zip(made, eager))
+        assert torch.equal(held[1], new[1]) and int(held[1].max()) < int((held[1] >= 0).sum())
+        # the attention is the same before and after its pages have moved
+        assert torch.equal(made[0], made[2]) and torch.equal(made[1], made[3])
+        live = held[1][held[1] >= 0].long()
+        assert torch.equal(held[0][live], new[0][live])
+
+
+def test_calls_of_every_kind_from_two_threads():
+    """Appends, rotations, copies and compactions at once: each thread's own buffers come out as they do alone."""
+    f = freqs_of(64).to(DEV)
+
+    def job(seed):
+        g = gen(seed)
+        i32 = dict(dtype=torch.int32, device=DEV)
+        cache = torch.randn(40, 16, 576, generator=g).to(DEV, torch.bfloat16)
+        kv, q = torch.randn(6, 576, generator=g).to(DEV, torch.bfloat16), torch.randn(6, 8, 576, generator=g).to(DEV, torch.bfloat16)
+        table = torch.randperm(40, generator=g)[:12].int().view(2, 6).to(DEV)
+        lens = torch.tensor([70, 33], **i32)
+        src, dst = torch.randperm(40, generator=g)[:30].int().to(DEV), torch.randperm(40, generator=g)[:30].int().to(DEV)
+
+        def once():
+            c, p = cache.clone(), q.clone()
+            kda.kda_latent_append(kv, c, table, lens, q_pe=p[..., 512:], q=p, freqs=f)
+            kda.kda_pages_copy(c, src, dst)
+            names = kda.kda_pages_compact(c, table)
+            return c[names.long()], p, names, kda.kda_rope(p, torch.arange(6, **i32), f, offset=8)
+
+        want = once()
+        torch.cuda.synchronize()
+        return lambda: None if all(torch.equal(a, b) for a, b in zip(once(), want)) else "another answer"
+
+    assert not both_at_once([job(1), job(2)])
+    assert kda.kda_get_device_error() == 0
