@@ -589,8 +589,9 @@ def kda_latent_attn(q, cache, page_table, kv_lens, dv: int = 512, cu_seqlens=Non
     already holds them.  q [T,H,dk] bf16; cache [num_pages,page_size,dk] (pages
     may be strided), its first dv channels the values; page_table
     [N,max_pages], kv_lens [N] (new tokens included), cu_seqlens [N+1] or None
-    (T / N tokens each), all int32.  scale: default dk ** -0.5.  causal: a token
-    sees the keys up to its own position, else all of its sequence's.
+    (T / N tokens each), all int32.  scale: pass the layer's own, (width of an
+    expanded head) ** -0.5; the default dk ** -0.5 is that of the cached width, which
+    a layer with folded-in heads does not have.  causal: a token sees the keys up to its own position, else all of its sequence's.
     Returns (out [T,H,dv], lse [T,H] fp32); where they are allocated here, rows
     behind the last sequence are unspecified."""
     return (_ext or _load_ext()).latent_attn(q, cache, page_table, kv_lens, dv, cu_seqlens, out, lse, scale, causal)

@@ -41,8 +41,8 @@
 //     rest: the second product ends, its stages are loaded anew (2.6 thousand cycles,
 //     1.6 of them the TMA unit's 62 + 1.84 per 128 bytes for each box), S^T, softmax
 //     (1.0), again the second product: 3.5 thousand a tile, where the products alone
-//     take 1.9.  4 sequences of up to 500 tokens behind up to 8192 keys: 762 us in
-//     pages of 64 (680 TFLOP/s, 41% of the measured dense rate), 859 in pages of 16, whose
+//     take 1.9.  4 sequences of up to 500 tokens behind up to 8192 keys: 757 us in
+//     pages of 64 (685 TFLOP/s, 41% of the measured dense rate), 861 in pages of 16, whose
 //     boxes are a quarter as long.
 //   128-key tiles (one in flight) took 95 us and 1.19 ms; one warp for both products
 //     115 us and 1.45 ms.
@@ -60,8 +60,10 @@ constexpr int KT = 64;                        // keys of a tile
 // The reference m of a row's exponentials is the maximum of its first tile, and
 // is raised only when a later logit lies above it by more than TH powers of two: P up to
 // 2^TH keeps its relative precision in bf16, and O up to 2^TH kv_len max |c| in fp32 as long
-// as that is finite, hence the header's bound on kv_len times a value, 2^110.  (60 had
-// the same times, and overflowed from values of 2^67 on.)
+// as that is finite, hence the header's bound on kv_len times a value, 2^110.  (60
+// overflowed from values of 2^67 on.  The times are the same for logits of a standard
+// deviation of up to 7.5 powers of two; at 25 and 100 the 4 chunks take 872 and 884 us, with
+// 60 861 and 876, and 64 sequences 77.8 and 79.8 with either.)
 constexpr float TH = 16.f;
 // What a row tile costs besides its key tiles, in key tiles: 32 sequences x 4 tokens
 // up to 8000 keys take 101 us with 0, 93.7 with 1, 88 with 2, 84.6 with 4, 87.8 with 8;
@@ -725,6 +727,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
 #pragma unroll
                 for (int c = 0; c < 16; ++c) x[c] = prep::ex2_approx(y[c]);
+                // P in bf16, the type of C beside it in the product; the sums l are of the unrounded ones.  Against 64
+                // bits the output is off by 2.1e-3 (norm), where a form in 32 bits rounded once has 1.7e-3.
                 unsigned char *P = sm + L::P_OFF;
 #pragma unroll
                 for (int g = 0; g < 2; ++g)

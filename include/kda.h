@@ -513,10 +513,13 @@ kda_status kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  *   rows below it must be finite, as must q (of the tokens that count) and the
  *   logits x_j, above -1e30; the largest magnitude of a value times kv_len must
  *   stay below 2^110 (sums are formed in fp32, of probabilities up to 2^16).  A
- *   NaN that a row sees all the same shows as NaN in its out and lse.
+ *   NaN that a row sees all the same shows as NaN in its out and lse, and may
+ *   show in the out of other rows of its sequence.
  * Deterministic: the same call gives the same bits.
  * Memory: a stream-ordered workspace from the library's pool, of a size that
  *   depends on the device, H, T / num_seqs and dv only (at most 39 MB).
+ * scale: that of the layer whose heads were folded into q; with the cached
+ *   width dk it has nothing to do.
  * Supported: KDA_BF16; dv in {256, 512}, dk - dv in {0, 64}; num_seqs <= 65535.
  *   q, cache, out 16-byte aligned, lse 4.  out must not overlap any input.
  */
@@ -532,7 +535,7 @@ kda_status kda_latent_attn(const void *q, const void *cache, const int32_t *page
  * channels, pair i (0 <= i < rot / 2) is turned by the angle
  *     a = position * freqs[i]      (off by at most 2^-24 pi, at any position)
  *     (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a)
- * and rounded once.  Pair i is channels (i, i + rot / 2), or (2i, 2i + 1) with
+ * in fp32, and rounded to dtype at the end.  Pair i is channels (i, i + rot / 2), or (2i, 2i + 1) with
  * KDA_ROPE_INTERLEAVED.  freqs: device float32 [rot / 2], so any base and any
  * scaling for long contexts is the caller's table; scale is their attention
  * factor.  KDA_ROPE_INVERSE turns by -a: with the same scale this is the
